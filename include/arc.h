@@ -285,6 +285,127 @@ arc_status arc_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_sf, const uin
                           int64_t ld_add, arc_stream_t stream);
 
 /* ----------------------------------------------------------------------------------------- */
+/* Mixture-of-experts layers: tokens sorted by expert and back, and the experts' products        */
+/* ----------------------------------------------------------------------------------------- */
+/*
+ * The pages' linear layers inside a mixture-of-experts block: each of T tokens goes to k of E
+ * experts. A slot is one (token, choice) pair, slot = token * k + choice; there are S = T * k.
+ * Sorted tensors hold one row per slot that has an expert, by ascending expert and, within one
+ * expert, by ascending slot. Slots whose id lies outside [0, E) have no expert: they get no row,
+ * add nothing and receive no gradient. Rows of a sorted tensor behind the last row in use are
+ * neither read for a result nor written.
+ *
+ * Plan (int32, device memory, arc_expert_plan_bytes bytes, 16-byte aligned), written by
+ * arc_expert_plan and read by every call below; its sections follow one another, each beginning at
+ * a multiple of 64 values:
+ *   offsets     [E + 1]  expert e owns sorted rows offsets[e] .. offsets[e + 1] - 1
+ *   blocks      [E + 1]  expert e's first 128-row block of scale bytes (exclusive sum of
+ *                        ceil(rows of e / 128))
+ *   row_of_slot [S]      the slot's sorted row, or -1
+ *   slot_of_row [S]      the row's slot; -1 behind the last row in use
+ *   sf_row      [S]      the row's place in the scale layout, 128 * blocks[e] + row - offsets[e];
+ *                        -1 behind the last row in use
+ *
+ * MXFP4 operands in sorted order: codes [S, K_pad/2] by sorted row; scale bytes in the 512-byte
+ * atoms of arc_quantize_act_mxfp4, but by sf_row, so that every expert begins a new 128-row block
+ * (arc_expert_sf_bytes bytes). Scale bytes of places that no row has are left as they were.
+ * Packed weights of E experts: codes [E * N, K_pad/2]; scale bytes of expert e at
+ * e * arc_mxfp4_sf_bytes(N, K + r).
+ *
+ * Limits of every call of this section: 1 <= E <= 1024, 1 <= k <= 1024, 1 <= T, S <= 2^28.
+ */
+size_t arc_expert_plan_bytes(int64_t tokens, int32_t k, int32_t experts);
+/* Bytes of the scale layout of S sorted rows of k_aug channels: (the most 128-row blocks that S
+ * slots of E experts can take, floor((S + 127 * min(E, S)) / 128)) * ceil(K_pad/128) * 512. */
+size_t arc_expert_sf_bytes(int64_t tokens, int32_t k, int32_t experts, int64_t k_aug);
+
+/*
+ * The plan of expert ids [T, k] (leading dimension ld_ids elements; id_bytes = 4 for int32, 8 for
+ * int64). One launch; equal ids give equal plans.
+ */
+arc_status arc_expert_plan(const void* ids, int32_t id_bytes, int64_t ld_ids, int64_t tokens, int32_t k,
+                           int32_t experts, int32_t* plan, size_t plan_bytes, arc_stream_t stream);
+
+/*
+ * rows [S, d] = tokens x [T, d] in sorted order (bf16 copies). d % 8 == 0, leading dimensions
+ * multiples of 8, 16-byte aligned pointers; here and below.
+ */
+arc_status arc_dispatch_experts_bf16(const void* x_bf16, int64_t ldx, int64_t d, const int32_t* plan, int64_t tokens,
+                                     int32_t k, int32_t experts, void* rows_bf16, int64_t ld_rows,
+                                     arc_stream_t stream);
+
+/* Its gradient: d_x [T, d] = bf16( sum over the token's rows of d_rows ), in fp32, by ascending
+ * choice; 0 for a token without rows. */
+arc_status arc_dispatch_experts_grad_bf16(const void* d_rows_bf16, int64_t ld_rows, int64_t d, const int32_t* plan,
+                                          int64_t tokens, int32_t k, int32_t experts, void* d_x_bf16, int64_t ldx,
+                                          arc_stream_t stream);
+
+/*
+ * y [T, d] = bf16( sum_j weights[t, j] * rows[row_of_slot[t k + j]] [+ add] ), in fp32, by
+ * ascending choice (then the addend); a token without rows gives 0 (+ add). weights fp32 [T, k]
+ * with leading dimension ld_weights; the weight of a slot without a row is not used. add_bf16 NULL
+ * or [T, d]; it may alias y.
+ */
+arc_status arc_combine_experts_bf16(const void* rows_bf16, int64_t ld_rows, int64_t d, const float* weights,
+                                    int64_t ld_weights, const int32_t* plan, int64_t tokens, int32_t k,
+                                    int32_t experts, const void* add_bf16, int64_t ld_add, void* y_bf16, int64_t ldy,
+                                    arc_stream_t stream);
+
+/*
+ * Its gradients from d_y [T, d] (the addend's is d_y itself): d_rows [S, d] =
+ * bf16(weights[t, j] * d_y[t]) and d_weights fp32 [T, k] (leading dimension ld_dw) =
+ * <d_y[t], rows[row]>, fp32 sums in a fixed order; 0 for a slot without a row. d_rows may alias
+ * rows.
+ */
+arc_status arc_combine_experts_grad_bf16(const void* d_y_bf16, int64_t ld_dy, const void* rows_bf16, int64_t ld_rows,
+                                         int64_t d, const float* weights, int64_t ld_weights, const int32_t* plan,
+                                         int64_t tokens, int32_t k, int32_t experts, void* d_rows_bf16,
+                                         int64_t ld_drows, float* d_weights, int64_t ld_dw, arc_stream_t stream);
+
+/*
+ * Tokens X [T, K] quantized as arc_quantize_act_mxfp4 would (r residual channels of d_idx
+ * included), each token once, its codes and scale bytes written to all its sorted rows. No bf16
+ * copy of the sorted rows is made. Requires K % 32 == 0, r % 32 == 0, 0 <= r <= K <= 2^20,
+ * r <= 32736.
+ */
+arc_status arc_quantize_act_experts_mxfp4(const void* x_bf16, int64_t ldx, int64_t K, const int32_t* d_idx, int32_t r,
+                                          const int32_t* plan, int64_t tokens, int32_t k, int32_t experts,
+                                          uint8_t* codes, uint8_t* sf, arc_stream_t stream);
+
+/*
+ * The input of the experts' down projection: sorted rows gu [S, 2F] (gate columns first) give
+ * act [S, F] = bf16( silu(gate) * up ), as arc_silu_mul_bf16, quantized as arc_quantize_act_mxfp4
+ * with r residual channels of d_idx (channels of act). One kernel; act is not written. Requires
+ * F % 32 == 0 and r as above.
+ */
+arc_status arc_quantize_swiglu_experts_mxfp4(const void* gu_bf16, int64_t ld_gu, int64_t F, const int32_t* d_idx,
+                                             int32_t r, const int32_t* plan, int64_t tokens, int32_t k,
+                                             int32_t experts, uint8_t* codes, uint8_t* sf, arc_stream_t stream);
+
+/* Weights [E, N, K] (experts one after another, row stride ldw) packed expert by expert as
+ * arc_pack_weight_mxfp4 packs one: E * N * K_pad / 2 code bytes, E * arc_mxfp4_sf_bytes(N, K + r)
+ * scale bytes. */
+arc_status arc_pack_weight_experts_mxfp4(const void* w_bf16, int32_t experts, int64_t N, int64_t K, int64_t ldw,
+                                         const int32_t* d_idx, int32_t r, uint8_t* codes, uint8_t* sf,
+                                         arc_stream_t stream);
+
+/*
+ * Y [S, N] bf16 = each sorted row times its expert's weights: bf16_rn( sum_{k < K_pad} E2M1(a) X_A
+ * * E2M1(b) X_B ), one launch over all experts, fp32 accumulation in tensor memory. A from the two
+ * quantizers above, B from arc_pack_weight_experts_mxfp4. N % 8 == 0, ldy % 8 == 0.
+ */
+arc_status arc_gemm_experts_mxfp4(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* b_codes,
+                                  const uint8_t* b_sf, const int32_t* plan, int64_t tokens, int32_t k,
+                                  int32_t experts, int64_t N, int64_t k_aug, void* y_bf16, int64_t ldy,
+                                  arc_stream_t stream);
+
+/* The BF16 switch of the same product: Y [S, N] = bf16_rn(rows W_e^T), rows [S, K], W [E, N, K]
+ * (experts one after another, row stride ldw). K % 8 == 0, N % 8 == 0. */
+arc_status arc_gemm_experts_bf16(const void* rows_bf16, int64_t ld_rows, const void* w_bf16, int64_t ldw,
+                                 const int32_t* plan, int64_t tokens, int32_t k, int32_t experts, int64_t N,
+                                 int64_t K, void* y_bf16, int64_t ldy, arc_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------- */
 /* Elementwise pieces of the recurrent SwiGLU block                                            */
 /* ----------------------------------------------------------------------------------------- */
 

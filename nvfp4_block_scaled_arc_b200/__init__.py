@@ -115,6 +115,45 @@ _SIGS = {
                                     ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
                                     ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                     ctypes.c_int64, ctypes.c_void_p]),
+    "arc_expert_plan_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]),
+    "arc_expert_sf_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64]),
+    "arc_expert_plan": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
+                                       ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
+                                       ctypes.c_void_p]),
+    "arc_dispatch_experts_bf16": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                                 ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                                 ctypes.c_int64, ctypes.c_void_p]),
+    "arc_dispatch_experts_grad_bf16": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                                      ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                                      ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "arc_combine_experts_bf16": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                                ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                                ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                                ctypes.c_int64, ctypes.c_void_p]),
+    "arc_combine_experts_grad_bf16": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                                     ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                                     ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                                     ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                                     ctypes.c_void_p]),
+    "arc_quantize_act_experts_mxfp4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                                      ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+                                                      ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                                      ctypes.c_void_p, ctypes.c_void_p]),
+    "arc_quantize_swiglu_experts_mxfp4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                                         ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                                         ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "arc_pack_weight_experts_mxfp4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
+                                                     ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                                     ctypes.c_void_p, ctypes.c_void_p]),
+    "arc_gemm_experts_mxfp4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                              ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                              ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                              ctypes.c_void_p]),
+    "arc_gemm_experts_bf16": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                             ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                             ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                             ctypes.c_void_p]),
     "arc_last_device_status": (ctypes.c_int, [ctypes.c_void_p]),
     "arc_set_wait_limit_ns": (ctypes.c_int, [ctypes.c_uint64]),
     "arc_debug_inject": (ctypes.c_int, [ctypes.c_int32]),
@@ -497,6 +536,323 @@ def gemm_fp8(a: FP8Tensor, b: FP8Tensor, out: torch.Tensor | None = None, add: t
     _check("arc_gemm_fp8", lib().arc_gemm_fp8(
         _p(a.codes), a.codes.stride(0), _p(a.scale), _p(b.codes), b.codes.stride(0), _p(b.scale), M, N, K,
         _p(out), out.stride(0), _p(add), 0 if add is None else add.stride(0), _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------------------------------------
+# Mixture-of-experts layers
+# ---------------------------------------------------------------------------------------------
+
+
+def _pad64(n: int) -> int:
+    return (n + 63) // 64 * 64
+
+
+class ExpertPlan:
+    """The slots (token * k + choice) sorted stably by expert: one int32 device buffer with the
+    sections that include/arc.h describes, seen through offsets, blocks, row_of_slot, slot_of_row and
+    sf_row. Made by expert_plan, or put around a buffer of that layout."""
+
+    __slots__ = ("buf", "tokens", "k", "experts")
+
+    def __init__(self, buf: torch.Tensor, tokens: int, k: int, experts: int):
+        if buf.numel() < 2 * _pad64(experts + 1) + 3 * _pad64(tokens * k) or not buf.is_contiguous():
+            raise ValueError("ExpertPlan: the buffer does not hold a plan of these sizes")
+        self.buf, self.tokens, self.k, self.experts = buf, tokens, k, experts
+
+    @property
+    def slots(self) -> int:
+        return self.tokens * self.k
+
+    def _section(self, i: int, n: int) -> torch.Tensor:
+        head = _pad64(self.experts + 1)
+        at = i * head if i < 2 else 2 * head + (i - 2) * _pad64(self.slots)
+        return self.buf[at:at + n]
+
+    offsets = property(lambda self: self._section(0, self.experts + 1))
+    blocks = property(lambda self: self._section(1, self.experts + 1))
+    row_of_slot = property(lambda self: self._section(2, self.slots))
+    slot_of_row = property(lambda self: self._section(3, self.slots))
+    sf_row = property(lambda self: self._section(4, self.slots))
+
+
+@dataclass
+class ExpertMXFP4:
+    """Sorted rows in MXFP4: codes [S, K_pad/2] u8 and scale bytes whose 128-row blocks begin anew
+    with every expert. k_aug = K + r."""
+    codes: torch.Tensor
+    sf: torch.Tensor
+    rows: int
+    k_aug: int
+
+
+@dataclass
+class ExpertWeightMXFP4:
+    """Packed weights of all experts: codes [E * N, K_pad/2] u8 and their scale bytes."""
+    codes: torch.Tensor
+    sf: torch.Tensor
+    experts: int
+    n: int
+    k_aug: int
+
+
+def _raw_stream(device: torch.device, stream) -> int:
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+
+
+class _on:
+    """The device of a call's tensors as the current one, and the caller's stream (if one is given)
+    as the one that its outputs are allocated for."""
+
+    __slots__ = ("ctx",)
+
+    def __init__(self, device: torch.device, stream):
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+        else:
+            self.ctx = None
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _expert_args(fn: str, device: torch.device, stream, **tensors):
+    """Refuses tensors (name = (tensor, dtype, shape or None)) that are not what fn takes: on the
+    call's device, of the dtype and shape, with consecutive values in a row."""
+    if device.type != "cuda":
+        raise ValueError(f"{fn}: tensors must be CUDA tensors")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {device}")
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{fn}: {name} is on {t.device}, not on {device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{fn}: {name} must be {list(shape)}, not {list(t.shape)}")
+        if t.stride(-1) != 1:
+            raise ValueError(f"{fn}: {name}'s rows must hold consecutive values")
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Leading dimension of [rows, cols]; a single row has the row's length, whatever its stride."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def expert_plan(ids: torch.Tensor, experts: int, out: ExpertPlan | None = None, stream=None) -> ExpertPlan:
+    """arc_expert_plan: the slots of expert ids [T, k] (int32 or int64) sorted by expert; ids outside
+    [0, experts) give their slots no row."""
+    dev = ids.device
+    if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 2:
+        raise ValueError("expert_plan: ids must be [tokens, k] of int32 or int64")
+    _expert_args("expert_plan", dev, stream, ids=(ids, ids.dtype, None),
+                 out=(None if out is None else out.buf, torch.int32, None))
+    T, k = ids.shape
+    with _on(dev, stream):
+        if out is None:
+            n = 2 * _pad64(experts + 1) + 3 * _pad64(T * k)
+            out = ExpertPlan(torch.empty(n, dtype=torch.int32, device=dev), T, k, experts)
+        elif (out.tokens, out.k, out.experts) != (T, k, experts):
+            raise ValueError("expert_plan: out was made for other sizes")
+        _check("arc_expert_plan", lib().arc_expert_plan(
+            ids.data_ptr(), ids.element_size(), _ld(ids), T, k, experts, out.buf.data_ptr(), out.buf.numel() * 4,
+            _raw_stream(dev, stream)))
+    return out
+
+
+def dispatch_experts(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """arc_dispatch_experts_bf16: tokens x [T, d] bf16 copied into sorted order [S, d]."""
+    dev, d = x.device, x.shape[-1]
+    _expert_args("dispatch_experts", dev, stream, x=(x, torch.bfloat16, (plan.tokens, d)),
+                 plan=(plan.buf, torch.int32, None), out=(out, torch.bfloat16, (plan.slots, d)))
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(plan.slots, d, dtype=torch.bfloat16, device=dev)
+        _check("arc_dispatch_experts_bf16", lib().arc_dispatch_experts_bf16(
+            x.data_ptr(), _ld(x), d, plan.buf.data_ptr(), plan.tokens, plan.k, plan.experts, out.data_ptr(), _ld(out),
+            _raw_stream(dev, stream)))
+    return out
+
+
+def dispatch_experts_grad(d_rows: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """arc_dispatch_experts_grad_bf16: the tokens' gradient [T, d] from the sorted rows' [S, d]."""
+    dev, d = d_rows.device, d_rows.shape[-1]
+    _expert_args("dispatch_experts_grad", dev, stream, d_rows=(d_rows, torch.bfloat16, (plan.slots, d)),
+                 plan=(plan.buf, torch.int32, None), out=(out, torch.bfloat16, (plan.tokens, d)))
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(plan.tokens, d, dtype=torch.bfloat16, device=dev)
+        _check("arc_dispatch_experts_grad_bf16", lib().arc_dispatch_experts_grad_bf16(
+            d_rows.data_ptr(), _ld(d_rows), d, plan.buf.data_ptr(), plan.tokens, plan.k, plan.experts, out.data_ptr(),
+            _ld(out), _raw_stream(dev, stream)))
+    return out
+
+
+def combine_experts(rows: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan, add: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """arc_combine_experts_bf16: y [T, d] = sum over the token's choices of weights [T, k] (fp32) times
+    the sorted rows [S, d] (+ add [T, d])."""
+    dev, d = rows.device, rows.shape[-1]
+    _expert_args("combine_experts", dev, stream, rows=(rows, torch.bfloat16, (plan.slots, d)),
+                 weights=(weights, torch.float32, (plan.tokens, plan.k)), plan=(plan.buf, torch.int32, None),
+                 add=(add, torch.bfloat16, (plan.tokens, d)), out=(out, torch.bfloat16, (plan.tokens, d)))
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(plan.tokens, d, dtype=torch.bfloat16, device=dev)
+        _check("arc_combine_experts_bf16", lib().arc_combine_experts_bf16(
+            rows.data_ptr(), _ld(rows), d, weights.data_ptr(), _ld(weights), plan.buf.data_ptr(), plan.tokens, plan.k,
+            plan.experts, None if add is None else add.data_ptr(), 0 if add is None else _ld(add), out.data_ptr(),
+            _ld(out), _raw_stream(dev, stream)))
+    return out
+
+
+def combine_experts_grad(d_y: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
+                         d_rows: torch.Tensor | None = None, d_weights: torch.Tensor | None = None,
+                         stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """arc_combine_experts_grad_bf16: (d_rows [S, d] bf16, d_weights [T, k] fp32) from d_y [T, d];
+    d_rows may be rows."""
+    dev, d = rows.device, rows.shape[-1]
+    _expert_args("combine_experts_grad", dev, stream, d_y=(d_y, torch.bfloat16, (plan.tokens, d)),
+                 rows=(rows, torch.bfloat16, (plan.slots, d)),
+                 weights=(weights, torch.float32, (plan.tokens, plan.k)), plan=(plan.buf, torch.int32, None),
+                 d_rows=(d_rows, torch.bfloat16, (plan.slots, d)),
+                 d_weights=(d_weights, torch.float32, (plan.tokens, plan.k)))
+    with _on(dev, stream):
+        if d_rows is None:
+            d_rows = torch.empty(plan.slots, d, dtype=torch.bfloat16, device=dev)
+        if d_weights is None:
+            d_weights = torch.empty(plan.tokens, plan.k, dtype=torch.float32, device=dev)
+        _check("arc_combine_experts_grad_bf16", lib().arc_combine_experts_grad_bf16(
+            d_y.data_ptr(), _ld(d_y), rows.data_ptr(), _ld(rows), d, weights.data_ptr(), _ld(weights),
+            plan.buf.data_ptr(), plan.tokens, plan.k, plan.experts, d_rows.data_ptr(), _ld(d_rows),
+            d_weights.data_ptr(), _ld(d_weights), _raw_stream(dev, stream)))
+    return d_rows, d_weights
+
+
+def _expert_mx_out(plan: ExpertPlan, k_aug: int, device) -> ExpertMXFP4:
+    codes = torch.empty(plan.slots, (k_aug + 63) // 64 * 32, dtype=torch.uint8, device=device)
+    sf = torch.empty(lib().arc_expert_sf_bytes(plan.tokens, plan.k, plan.experts, k_aug), dtype=torch.uint8,
+                     device=device)
+    return ExpertMXFP4(codes, sf, plan.slots, k_aug)
+
+
+def _expert_quantize(fn: str, x: torch.Tensor, plan: ExpertPlan, K: int, idx, out: ExpertMXFP4 | None, stream,
+                     rows: int):
+    dev = x.device
+    r = 0 if idx is None else idx.numel()
+    _expert_args(fn, dev, stream, x=(x, torch.bfloat16, (rows, x.shape[-1])), plan=(plan.buf, torch.int32, None),
+                 idx=(idx, torch.int32, None), codes=(None if out is None else out.codes, torch.uint8, None),
+                 sf=(None if out is None else out.sf, torch.uint8, None))
+    if out is not None and (out.rows != plan.slots or out.k_aug != K + r or
+                            out.codes.numel() < codes_bytes(plan.slots, K + r) or
+                            out.sf.numel() < lib().arc_expert_sf_bytes(plan.tokens, plan.k, plan.experts, K + r)):
+        raise ValueError(f"{fn}: out was made for other sizes")
+    with _on(dev, stream):
+        if out is None:
+            out = _expert_mx_out(plan, K + r, dev)
+        _check("arc_" + fn, getattr(lib(), "arc_" + fn)(
+            x.data_ptr(), _ld(x), K, None if idx is None else idx.data_ptr(), r, plan.buf.data_ptr(), plan.tokens,
+            plan.k, plan.experts, out.codes.data_ptr(), out.sf.data_ptr(), _raw_stream(dev, stream)))
+    return out
+
+
+def quantize_act_experts_mxfp4(x: torch.Tensor, plan: ExpertPlan, idx: torch.Tensor | None = None,
+                               out: ExpertMXFP4 | None = None, stream=None) -> ExpertMXFP4:
+    """arc_quantize_act_experts_mxfp4: tokens x [T, K] bf16 in MXFP4 with r appended residual channels,
+    written to their sorted rows."""
+    return _expert_quantize("quantize_act_experts_mxfp4", x, plan, x.shape[-1], idx, out, stream, plan.tokens)
+
+
+def quantize_swiglu_experts_mxfp4(gu: torch.Tensor, plan: ExpertPlan, idx: torch.Tensor | None = None,
+                                  out: ExpertMXFP4 | None = None, stream=None) -> ExpertMXFP4:
+    """arc_quantize_swiglu_experts_mxfp4: silu(gate) * up of the sorted rows gu [S, 2F], in MXFP4."""
+    if gu.shape[-1] % 2:
+        raise ValueError("quantize_swiglu_experts_mxfp4: gu must have as many gate as up columns")
+    return _expert_quantize("quantize_swiglu_experts_mxfp4", gu, plan, gu.shape[-1] // 2, idx, out, stream, plan.slots)
+
+
+def pack_weight_experts_mxfp4(w: torch.Tensor, idx: torch.Tensor | None = None, out: ExpertWeightMXFP4 | None = None,
+                              stream=None) -> ExpertWeightMXFP4:
+    """arc_pack_weight_experts_mxfp4: W [E, N, K] bf16 (experts one after another) -> MXFP4 of
+    [W_e | W_e[:, idx]] for every expert."""
+    dev = w.device
+    if w.dim() != 3:
+        raise ValueError("pack_weight_experts_mxfp4: w must be [experts, N, K]")
+    E, N, K = w.shape
+    r = 0 if idx is None else idx.numel()
+    _expert_args("pack_weight_experts_mxfp4", dev, stream, w=(w, torch.bfloat16, None), idx=(idx, torch.int32, None))
+    ld = _expert_weight_ld("pack_weight_experts_mxfp4", w)
+    cb, sb = E * codes_bytes(N, K + r), E * mxfp4_sf_bytes(N, K + r)
+    if out is not None and ((out.experts, out.n, out.k_aug) != (E, N, K + r) or out.codes.numel() < cb or
+                            out.sf.numel() < sb or out.codes.device != dev or out.sf.device != dev):
+        raise ValueError("pack_weight_experts_mxfp4: out was made for other sizes")
+    with _on(dev, stream):
+        if out is None:
+            out = ExpertWeightMXFP4(torch.empty(E * N, cb // max(E * N, 1), dtype=torch.uint8, device=dev),
+                                    torch.empty(sb, dtype=torch.uint8, device=dev), E, N, K + r)
+        _check("arc_pack_weight_experts_mxfp4", lib().arc_pack_weight_experts_mxfp4(
+            w.data_ptr(), E, N, K, ld, None if idx is None else idx.data_ptr(), r, out.codes.data_ptr(),
+            out.sf.data_ptr(), _raw_stream(dev, stream)))
+    return out
+
+
+def _expert_weight_ld(fn: str, w: torch.Tensor) -> int:
+    E, N, K = w.shape
+    ld = w.stride(1) if N > 1 else (w.stride(0) if E > 1 else K)
+    if E > 1 and w.stride(0) != N * ld:
+        raise ValueError(f"{fn}: the experts' weights must lie one after another")
+    return ld
+
+
+def gemm_experts_mxfp4(a: ExpertMXFP4, w: ExpertWeightMXFP4, plan: ExpertPlan, out: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """arc_gemm_experts_mxfp4: Y [S, N] bf16 = each sorted row times its expert's weights."""
+    dev = a.codes.device
+    if a.k_aug != w.k_aug or w.experts != plan.experts or a.rows != plan.slots:
+        raise ValueError("gemm_experts_mxfp4: operands of other sizes than the plan's, or of two depths")
+    if (a.codes.numel() < codes_bytes(a.rows, a.k_aug) or w.codes.numel() < codes_bytes(w.experts * w.n, w.k_aug) or
+            a.sf.numel() < lib().arc_expert_sf_bytes(plan.tokens, plan.k, plan.experts, a.k_aug) or
+            w.sf.numel() < w.experts * mxfp4_sf_bytes(w.n, w.k_aug)):
+        raise ValueError("gemm_experts_mxfp4: an operand's buffer is smaller than its sizes say")
+    _expert_args("gemm_experts_mxfp4", dev, stream, a_codes=(a.codes, torch.uint8, None),
+                 a_sf=(a.sf, torch.uint8, None), w_codes=(w.codes, torch.uint8, None), w_sf=(w.sf, torch.uint8, None),
+                 plan=(plan.buf, torch.int32, None), out=(out, torch.bfloat16, (plan.slots, w.n)))
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(plan.slots, w.n, dtype=torch.bfloat16, device=dev)
+        _check("arc_gemm_experts_mxfp4", lib().arc_gemm_experts_mxfp4(
+            a.codes.data_ptr(), a.sf.data_ptr(), w.codes.data_ptr(), w.sf.data_ptr(), plan.buf.data_ptr(), plan.tokens,
+            plan.k, plan.experts, w.n, a.k_aug, out.data_ptr(), _ld(out), _raw_stream(dev, stream)))
+    return out
+
+
+def gemm_experts_bf16(rows: torch.Tensor, w: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """arc_gemm_experts_bf16: Y [S, N] = bf16 of each sorted row [S, K] times its expert's W [E, N, K]."""
+    dev, K = rows.device, rows.shape[-1]
+    if w.dim() != 3:
+        raise ValueError("gemm_experts_bf16: w must be [experts, N, K]")
+    N = w.shape[1]
+    _expert_args("gemm_experts_bf16", dev, stream, rows=(rows, torch.bfloat16, (plan.slots, K)),
+                 w=(w, torch.bfloat16, (plan.experts, N, K)), plan=(plan.buf, torch.int32, None),
+                 out=(out, torch.bfloat16, (plan.slots, N)))
+    ld = _expert_weight_ld("gemm_experts_bf16", w)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(plan.slots, N, dtype=torch.bfloat16, device=dev)
+        _check("arc_gemm_experts_bf16", lib().arc_gemm_experts_bf16(
+            rows.data_ptr(), _ld(rows), w.data_ptr(), ld, plan.buf.data_ptr(), plan.tokens, plan.k, plan.experts, N, K,
+            out.data_ptr(), _ld(out), _raw_stream(dev, stream)))
     return out
 
 

@@ -1,0 +1,488 @@
+// experts.cuh -- the memory-bound kernels of mixture-of-experts layers: the plan (a stable counting
+// sort of the slots by expert), tokens copied into sorted order and summed back with their router
+// weights, the gradients of both, and the MXFP4 quantizers that write sorted rows.
+//
+// Slot s = token * k + choice; offsets[e] is the first sorted row of expert e, blocks[e] its first
+// 128-row block of scale bytes. Sorted rows are dense (no padding between experts), so everything
+// here moves only rows that exist; the scale bytes alone begin a new 128-row block per expert,
+// because the block-scaled GEMM reads them by 128-row atoms.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "elementwise.cuh"
+
+namespace arc {
+
+constexpr int kMaxExperts = 1024;
+
+// Sections of the plan, each beginning at a multiple of 64 values.
+__host__ __device__ constexpr int64_t plan_pad(int64_t n) { return (n + 63) / 64 * 64; }
+
+struct Plan {
+  const int32_t* offsets;
+  const int32_t* blocks;
+  const int32_t* row_of_slot;
+  const int32_t* slot_of_row;
+  const int32_t* sf_row;
+};
+
+__host__ __device__ inline Plan plan_sections(const int32_t* p, int64_t slots, int experts) {
+  Plan v;
+  v.offsets = p;
+  v.blocks = v.offsets + plan_pad(experts + 1);
+  v.row_of_slot = v.blocks + plan_pad(experts + 1);
+  v.slot_of_row = v.row_of_slot + plan_pad(slots);
+  v.sf_row = v.slot_of_row + plan_pad(slots);
+  return v;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Plan. One cluster of CTAs (one CTA for few slots), so one launch: every warp owns a contiguous
+// range of slots and counts its ids per expert in shared memory; the CTAs exchange their counts
+// through distributed shared memory; a scan over the experts gives offsets and blocks; then every
+// warp walks its range again, 32 slots at a time, and ranks equal ids of the 32 by lane
+// (match.any), which keeps the order of slots within an expert: no atomics decide a place.
+// ---------------------------------------------------------------------------------------------
+
+constexpr int kPlanThreads = 1024, kPlanWarps = 32, kPlanMaxCtas = 8;
+
+// Dynamic shared memory: per-warp counts [32][E], the CTA's counts [E], row bases [E], and what
+// turns a row of an expert into its place in the scale layout [E].
+__host__ __device__ constexpr size_t plan_smem_bytes(int experts) {
+  return static_cast<size_t>(kPlanWarps + 3) * static_cast<size_t>(experts) * 4;
+}
+
+template <typename ID>
+__device__ __forceinline__ int expert_id(const ID* ids, int64_t ld, int k, int s, int experts) {
+  const int t = s / k;
+  const ID v = ids[t * ld + (s - t * k)];
+  return v >= 0 && v < experts ? static_cast<int>(v) : -1;
+}
+
+template <typename ID>
+__global__ void __launch_bounds__(kPlanThreads, 1)
+    k_expert_plan(const ID* __restrict__ ids, int64_t ld, int slots, int k, int experts, int32_t* plan) {
+  namespace cg = cooperative_groups;
+  extern __shared__ int32_t plan_sm[];
+  __shared__ int32_t scan_rows[kPlanWarps], scan_blocks[kPlanWarps];
+  cg::cluster_group cluster = cg::this_cluster();
+  pdl_launch_dependents();
+  int32_t* warp_counts = plan_sm;                     // [32][E]
+  int32_t* counts = plan_sm + kPlanWarps * experts;   // [E]
+  int32_t* base = counts + experts;                   // [E] first row of this CTA's slots of the expert
+  int32_t* sf_shift = base + experts;                 // [E] sf_row - row
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  for (int i = tid; i < kPlanWarps * experts; i += kPlanThreads) warp_counts[i] = 0;
+  pdl_wait();  // the ids may come from the kernel before
+  __syncthreads();
+
+  const int nwarps = ctas * kPlanWarps;
+  const int chunk = (slots + nwarps * 32 - 1) / (nwarps * 32) * 32;
+  const int64_t lo64 = static_cast<int64_t>(cta * kPlanWarps + warp) * chunk;
+  const int lo = static_cast<int>(lo64 < slots ? lo64 : slots);
+  const int hi = min(slots - lo, chunk) + lo;
+  int32_t* mine = warp_counts + warp * experts;
+  for (int s = lo + lane; s < hi; s += 128) {  // four independent loads in flight
+    int e[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) e[u] = s + 32 * u < hi ? expert_id(ids, ld, k, s + 32 * u, experts) : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (e[u] >= 0) atomicAdd(&mine[e[u]], 1);
+  }
+  __syncthreads();
+  int total = 0, before = 0;  // thread e < E: rows of expert e in all CTAs, and in the CTAs before
+  if (tid < experts) {
+    int run = 0;
+#pragma unroll 8
+    for (int w = 0; w < kPlanWarps; ++w) {
+      const int c = warp_counts[w * experts + tid];
+      warp_counts[w * experts + tid] = run;
+      run += c;
+    }
+    counts[tid] = run;
+  }
+  cluster.sync();
+  if (tid < experts) {
+    for (int c = 0; c < ctas; ++c) {
+      const int v = *cluster.map_shared_rank(counts + tid, c);
+      total += v;
+      if (c < cta) before += v;
+    }
+  }
+  // exclusive scan over the experts (E <= 1024: one thread each)
+  const int nblk = (total + 127) >> 7;
+  int rows_in = total, blocks_in = nblk;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xFFFFFFFFu, rows_in, o), b = __shfl_up_sync(0xFFFFFFFFu, blocks_in, o);
+    if (lane >= o) {
+      rows_in += a;
+      blocks_in += b;
+    }
+  }
+  if (lane == 31) {
+    scan_rows[warp] = rows_in;
+    scan_blocks[warp] = blocks_in;
+  }
+  __syncthreads();
+  int rows0 = 0, blocks0 = 0, all_rows = 0, all_blocks = 0;
+  for (int w = 0; w < kPlanWarps; ++w) {
+    const int a = scan_rows[w], b = scan_blocks[w];
+    if (w < warp) {
+      rows0 += a;
+      blocks0 += b;
+    }
+    all_rows += a;
+    all_blocks += b;
+  }
+  const int off = rows0 + rows_in - total, blk = blocks0 + blocks_in - nblk;
+  int32_t* g_offsets = plan;
+  int32_t* g_blocks = g_offsets + plan_pad(experts + 1);
+  int32_t* g_row_of_slot = g_blocks + plan_pad(experts + 1);
+  int32_t* g_slot_of_row = g_row_of_slot + plan_pad(slots);
+  int32_t* g_sf_row = g_slot_of_row + plan_pad(slots);
+  if (tid < experts) {
+    base[tid] = off + before;
+    sf_shift[tid] = 128 * blk - off;
+    if (cta == 0) {
+      g_offsets[tid] = off;
+      g_blocks[tid] = blk;
+      if (tid == 0) {
+        g_offsets[experts] = all_rows;
+        g_blocks[experts] = all_blocks;
+      }
+    }
+  }
+  __syncthreads();
+  for (int s0 = lo; s0 < hi; s0 += 32) {
+    const int s = s0 + lane;
+    const int e = s < hi ? expert_id(ids, ld, k, s, experts) : -1;
+    const uint32_t peers = __match_any_sync(0xFFFFFFFFu, e);
+    int row = -1;
+    if (e >= 0) row = base[e] + mine[e] + __popc(peers & ((1u << lane) - 1u));
+    __syncwarp();  // every lane has read its count before the first of each expert moves it on
+    if (e >= 0 && (peers & ((1u << lane) - 1u)) == 0u) mine[e] += __popc(peers);
+    __syncwarp();
+    if (s < hi) g_row_of_slot[s] = row;
+    if (e >= 0) {
+      g_slot_of_row[row] = s;
+      g_sf_row[row] = row + sf_shift[e];
+    }
+  }
+  for (int i = all_rows + cta * kPlanThreads + tid; i < slots; i += ctas * kPlanThreads) {
+    g_slot_of_row[i] = -1;
+    g_sf_row[i] = -1;
+  }
+  cluster.sync();  // no CTA leaves while another may still read its counts
+}
+
+// ---------------------------------------------------------------------------------------------
+// Sorted rows and back. A warp takes one token and a segment of 32 * U 16-byte vectors of it; lane
+// j holds the place (and weight) of choice j, broadcast by shuffle.
+// ---------------------------------------------------------------------------------------------
+
+constexpr int kMoveThreads = 256;
+
+template <int U>
+__global__ void __launch_bounds__(kMoveThreads) k_dispatch(const __nv_bfloat16* __restrict__ x, int64_t ldx, int vecs,
+                                                           Plan p, int64_t tokens, int k,
+                                                           __nv_bfloat16* __restrict__ rows, int64_t ldr) {
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int nseg = (vecs + 32 * U - 1) / (32 * U);
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
+  const int64_t t = task / nseg;
+  pdl_wait();
+  if (t >= tokens) return;
+  const int v0 = static_cast<int>(task - t * nseg) * 32 * U + lane;
+  uint4 w[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    w[u] = v0 + 32 * u < vecs ? ld_nc_v4(x + t * ldx + 8 * (v0 + 32 * u)) : make_uint4(0, 0, 0, 0);
+  for (int j0 = 0; j0 < k; j0 += 32) {
+    const int nj = min(32, k - j0);
+    const int mine = lane < nj ? p.row_of_slot[t * k + j0 + lane] : -1;
+    for (int j = 0; j < nj; ++j) {
+      const int64_t row = __shfl_sync(0xFFFFFFFFu, mine, j);
+      if (row < 0) continue;
+      uint4* dst = reinterpret_cast<uint4*>(rows + row * ldr);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v0 + 32 * u < vecs) dst[v0 + 32 * u] = w[u];
+    }
+  }
+}
+
+__device__ __forceinline__ void fma_bf16x8(float (&acc)[8], float w, uint4 v) {
+  acc[0] = __fmaf_rn(w, bf16_lo(v.x), acc[0]);
+  acc[1] = __fmaf_rn(w, bf16_hi(v.x), acc[1]);
+  acc[2] = __fmaf_rn(w, bf16_lo(v.y), acc[2]);
+  acc[3] = __fmaf_rn(w, bf16_hi(v.y), acc[3]);
+  acc[4] = __fmaf_rn(w, bf16_lo(v.z), acc[4]);
+  acc[5] = __fmaf_rn(w, bf16_hi(v.z), acc[5]);
+  acc[6] = __fmaf_rn(w, bf16_lo(v.w), acc[6]);
+  acc[7] = __fmaf_rn(w, bf16_hi(v.w), acc[7]);
+}
+
+// y[t] = bf16( sum_j w_j rows[row_j] [+ add] ): the combine, and with weights of one (weights ==
+// nullptr) the gradient of the dispatch.
+template <int U>
+__global__ void __launch_bounds__(kMoveThreads)
+    k_combine(const __nv_bfloat16* __restrict__ rows, int64_t ldr, int vecs, const float* __restrict__ weights,
+              int64_t ldw, Plan p, int64_t tokens, int k, const __nv_bfloat16* add, int64_t lda, __nv_bfloat16* y,
+              int64_t ldy) {
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int nseg = (vecs + 32 * U - 1) / (32 * U);
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
+  const int64_t t = task / nseg;
+  pdl_wait();
+  if (t >= tokens) return;
+  const int v0 = static_cast<int>(task - t * nseg) * 32 * U + lane;
+  float acc[U][8];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[u][i] = 0.0f;
+  for (int j0 = 0; j0 < k; j0 += 32) {
+    const int nj = min(32, k - j0);
+    const int mine = lane < nj ? p.row_of_slot[t * k + j0 + lane] : -1;
+    const float wmine = weights != nullptr && lane < nj ? weights[t * ldw + j0 + lane] : 1.0f;
+#pragma unroll 4
+    for (int j = 0; j < nj; ++j) {
+      const int64_t row = __shfl_sync(0xFFFFFFFFu, mine, j);
+      const float w = __shfl_sync(0xFFFFFFFFu, wmine, j);
+      if (row < 0) continue;
+      const __nv_bfloat16* src = rows + row * ldr;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v0 + 32 * u < vecs) fma_bf16x8(acc[u], w, ld_nc_v4(src + 8 * (v0 + 32 * u)));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int v = v0 + 32 * u;
+    if (v >= vecs) continue;
+    if (add != nullptr)
+      fma_bf16x8(acc[u], 1.0f, *reinterpret_cast<const uint4*>(add + t * lda + 8 * v));
+    *reinterpret_cast<uint4*>(y + t * ldy + 8 * v) =
+        make_uint4(pack_bf16x2_rn(acc[u][0], acc[u][1]), pack_bf16x2_rn(acc[u][2], acc[u][3]),
+                   pack_bf16x2_rn(acc[u][4], acc[u][5]), pack_bf16x2_rn(acc[u][6], acc[u][7]));
+  }
+}
+
+// One warp per slot: d_rows[row] = bf16(w d_y[t]) and d_w = <d_y[t], rows[row]> (fp32 partial sums
+// by lane, joined by shuffles: a fixed order). d_rows may be rows: each vector is read before the
+// same lane writes it.
+__global__ void __launch_bounds__(kMoveThreads)
+    k_combine_grad(const __nv_bfloat16* __restrict__ dy, int64_t lddy, const __nv_bfloat16* rows, int64_t ldr,
+                   int vecs, const float* __restrict__ weights, int64_t ldw, Plan p, int64_t tokens, int k,
+                   __nv_bfloat16* d_rows, int64_t lddr, float* __restrict__ d_w, int64_t lddw) {
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t s = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
+  pdl_wait();
+  if (s >= tokens * k) return;
+  const int64_t t = s / k, j = s - t * k;
+  const int64_t row = p.row_of_slot[s];
+  if (row < 0) {
+    if (lane == 0) d_w[t * lddw + j] = 0.0f;
+    return;
+  }
+  const float w = weights[t * ldw + j];
+  const __nv_bfloat16* a = dy + t * lddy;
+  const __nv_bfloat16* b = rows + row * ldr;
+  uint4* dst = reinterpret_cast<uint4*>(d_rows + row * lddr);
+  float dot = 0.0f;
+  constexpr int U = 4;  // vectors in flight: all loaded before the first is written (rows may be d_rows)
+  for (int v0 = lane; v0 < vecs; v0 += 32 * U) {
+    uint4 g[U], r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = v0 + 32 * u;
+      g[u] = r[u] = make_uint4(0, 0, 0, 0);
+      if (v < vecs) {
+        g[u] = ld_nc_v4_l1(a + 8 * v);
+        r[u] = *reinterpret_cast<const uint4*>(b + 8 * v);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t gs[4] = {g[u].x, g[u].y, g[u].z, g[u].w}, rs[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float g0 = bf16_lo(gs[i]), g1 = bf16_hi(gs[i]);
+        dot = __fmaf_rn(g0, bf16_lo(rs[i]), dot);
+        dot = __fmaf_rn(g1, bf16_hi(rs[i]), dot);
+        o[i] = pack_bf16x2_rn(__fmul_rn(w, g0), __fmul_rn(w, g1));
+      }
+      if (v0 + 32 * u < vecs) dst[v0 + 32 * u] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+  if (lane == 0) d_w[t * lddw + j] = dot;
+}
+
+// ---------------------------------------------------------------------------------------------
+// MXFP4 quantization into sorted order (format and arithmetic of k_quant_mx_rows). SRC tokens: the
+// row of a token is coded once and written to the token's k sorted rows. SRC SwiGLU: row i of
+// gate|up gives act = bf16(silu(gate) * up) (the arithmetic of k_silu_mul), coded into sorted row
+// i; act never goes to memory. A warp takes one task: 16 blocks of 32 values (lane pairs, as
+// k_quant_mx_rows), or one appended block of 32 outlier channels (a lane each: it forms its
+// channel's primary block's maximum again from the row, at most 64 more bytes from L1/L2 per
+// channel, so no two tasks of a row depend on each other and few tokens still fill the machine).
+// ---------------------------------------------------------------------------------------------
+
+constexpr int kQexTokens = 0, kQexSwiglu = 1;
+
+struct QuantExpertsArgs {
+  const __nv_bfloat16* x;  // tokens [T, K], or gate|up [S, 2 K]
+  int64_t ldx;
+  int64_t n;               // tokens, or slots
+  int K, r, kpad, katoms;  // katoms = ceil(K_pad / 128)
+  const int32_t* idx;
+  Plan p;
+  int k, experts;
+  uint8_t* codes;
+  uint8_t* sf;
+};
+
+// silu(g) * u of a bf16 pair each, rounded to bf16 (k_silu_mul's arithmetic).
+__device__ __forceinline__ uint32_t silu_mul_pair(uint32_t g, uint32_t u) {
+  const float g0 = bf16_lo(g), g1 = bf16_hi(g);
+  const float s0 = __fdiv_rn(g0, __fadd_rn(1.0f, expf(-g0))), s1 = __fdiv_rn(g1, __fadd_rn(1.0f, expf(-g1)));
+  return pack_bf16x2_rn(__fmul_rn(s0, bf16_lo(u)), __fmul_rn(s1, bf16_hi(u)));
+}
+
+// 16 consecutive values of the source row from channel c on, as 8 bf16 pairs.
+template <int SRC>
+__device__ __forceinline__ void load16(const __nv_bfloat16* row, int K, int c, uint32_t (&w)[8]) {
+  const uint4 a = ld_nc_v4_l1(row + c), b = ld_nc_v4_l1(row + c + 8);
+  const uint32_t g[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if constexpr (SRC == kQexSwiglu) {
+    const uint4 ua = ld_nc_v4_l1(row + K + c), ub = ld_nc_v4_l1(row + K + c + 8);
+    const uint32_t u[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = silu_mul_pair(g[i], u[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = g[i];
+  }
+}
+
+template <int SRC>
+__global__ void __launch_bounds__(256) k_quant_experts(QuantExpertsArgs a) {
+  pdl_launch_dependents();  // the GEMM that follows may set itself up meanwhile
+  const int lane = threadIdx.x & 31;
+  const int nblk = a.K >> 5, nseg = (nblk + 15) >> 4, nres = a.r >> 5;
+  const int ntask = nseg + nres;
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t src = task / ntask;
+  const int part = static_cast<int>(task - src * ntask);
+  pdl_wait();
+  if (src >= a.n) return;
+  if (SRC == kQexSwiglu && src >= a.p.offsets[a.experts]) return;
+  const __nv_bfloat16* row = a.x + src * a.ldx;
+  const int64_t cpitch = a.kpad >> 1;
+  const int nrows = SRC == kQexTokens ? a.k : 1;
+  // lane j: sorted row and scale place of the source row's j-th destination
+  auto places = [&](int j0, int& dst, int& sfr) {
+    dst = sfr = -1;
+    if (j0 + lane < nrows) {
+      dst = SRC == kQexTokens ? a.p.row_of_slot[src * a.k + j0 + lane] : static_cast<int>(src);
+      if (dst >= 0) sfr = a.p.sf_row[dst];
+    }
+  };
+  auto sf_base = [&](int64_t m) { return a.sf + (m >> 7) * a.katoms * 512 + (m & 31) * 16 + ((m >> 5) & 3) * 4; };
+  int dst0, sfr0;
+  places(0, dst0, sfr0);
+  if (part < nseg) {
+    const int half = lane & 1;
+    const int b = part * 16 + (lane >> 1);
+    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (b < nblk) load16<SRC>(row, a.K, 32 * b + 16 * half, w);
+    const uint32_t mine = __float_as_uint(absmax16_bf16(w));
+    const uint32_t am = max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
+    const uint32_t sb = mx_scale_byte(am);
+    uint64_t p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = f2_pack(bf16_lo(w[e]), bf16_hi(w[e]));
+    uint2 cc = mx_encode16(p, mx_inv_scale(sb));
+    if (am == 0u) cc = make_uint2(0u, 0u);
+    // the last segment also zeroes the columns behind the appended blocks
+    const int ncols = 4 * a.katoms, pad0 = nblk + nres;
+    const bool last = part == nseg - 1;
+    for (int j0 = 0; j0 < nrows; j0 += 32) {
+      if (j0) places(j0, dst0, sfr0);
+      const int nj = min(32, nrows - j0);
+      for (int j = 0; j < nj; ++j) {
+        const int64_t dst = __shfl_sync(0xFFFFFFFFu, dst0, j);
+        const int64_t m = __shfl_sync(0xFFFFFFFFu, sfr0, j);
+        if (dst < 0) continue;
+        uint8_t* crow = a.codes + dst * cpitch;
+        uint8_t* srow = sf_base(m);
+        if (b < nblk) {
+          *reinterpret_cast<uint2*>(crow + 16 * b + 8 * half) = cc;
+          if (!half) srow[(b >> 2) * 512 + (b & 3)] = static_cast<uint8_t>(sb);
+        }
+        if (last && pad0 + lane < ncols) {
+          const int kb = pad0 + lane;
+          if (16 * kb < cpitch) *reinterpret_cast<uint4*>(crow + 16 * kb) = make_uint4(0, 0, 0, 0);
+          srow[(kb >> 2) * 512 + (kb & 3)] = 0;
+        }
+      }
+    }
+  } else {
+    const int rb = part - nseg;
+    const int c = a.idx[32 * rb + lane];
+    float res = 0.0f;
+    if (static_cast<unsigned>(c) < static_cast<unsigned>(a.K)) {
+      uint32_t w[8], w2[8];
+      load16<SRC>(row, a.K, c & ~31, w);
+      load16<SRC>(row, a.K, (c & ~31) + 16, w2);
+      const uint32_t am = max(__float_as_uint(absmax16_bf16(w)), __float_as_uint(absmax16_bf16(w2)));
+      uint32_t pair = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i == ((c & 15) >> 1)) pair = (c & 16) ? w2[i] : w[i];
+      }
+      const float xv = (c & 1) ? bf16_hi(pair) : bf16_lo(pair);
+      res = xv;
+      if (am != 0u) {
+        const uint32_t t = mx_scale_byte(am);
+        float q[8] = {__fmul_rn(xv, mx_inv_scale(t)), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        res = __fsub_rn(xv, __fmul_rn(e2m1_value(e2m1x8_rn_sat(q) & 15u), mx_scale(t)));
+      }
+    } else if (src == 0) {
+      set_status(kStatusInvalidArg);
+    }
+    const uint32_t am = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(res)));
+    const uint32_t sb = mx_scale_byte(am);
+    float q[8] = {__fmul_rn(res, mx_inv_scale(sb)), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    uint32_t code = am == 0u ? 0u : e2m1x8_rn_sat(q) & 15u;
+    // eight lanes' codes make one 32-bit word, the first lane's lowest
+    code |= __shfl_down_sync(0xFFFFFFFFu, code, 1) << 4;
+    code |= __shfl_down_sync(0xFFFFFFFFu, code, 2) << 8;
+    code |= __shfl_down_sync(0xFFFFFFFFu, code, 4) << 16;
+    const int kb = nblk + rb;
+    for (int j0 = 0; j0 < nrows; j0 += 32) {
+      if (j0) places(j0, dst0, sfr0);
+      const int nj = min(32, nrows - j0);
+      for (int j = 0; j < nj; ++j) {
+        const int64_t dst = __shfl_sync(0xFFFFFFFFu, dst0, j);
+        const int64_t m = __shfl_sync(0xFFFFFFFFu, sfr0, j);
+        if (dst < 0) continue;
+        if ((lane & 7) == 0)
+          *reinterpret_cast<uint32_t*>(a.codes + dst * cpitch + 16 * kb + (lane >> 1)) = code;
+        if (lane == 1) sf_base(m)[(kb >> 2) * 512 + (kb & 3)] = static_cast<uint8_t>(sb);
+      }
+    }
+  }
+}
+
+}  // namespace arc

@@ -13,7 +13,9 @@
 
 #include "../../include/arc.h"
 #include "elementwise.cuh"
+#include "experts.cuh"
 #include "gemm.cuh"
+#include "gemm_experts.cuh"
 #include "quant.cuh"
 
 namespace {
@@ -68,6 +70,18 @@ arc_status device_check(int* sms) {
                              arc::gemm_smem_bytes<arc::kGemmMX4>()) != cudaSuccess ||
         cudaFuncSetAttribute(arc::k_gemm<arc::kGemmMX4, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              arc::gemm_smem_bytes<arc::kGemmMX4>()) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmMX4, 1>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmMX4, 2>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmBF16, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmBF16, 1>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmBF16, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmBF16, 2>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_expert_plan<int32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(arc::plan_smem_bytes(arc::kMaxExperts))) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_expert_plan<int64_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(arc::plan_smem_bytes(arc::kMaxExperts))) != cudaSuccess ||
         cudaFuncSetAttribute(arc::k_quant_mx_rows, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              arc::kQRowsSmemMax) != cudaSuccess ||
         cudaFuncSetAttribute(arc::k_quant_reordered<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -361,6 +375,146 @@ arc_status gemm_launch(const CUtensorMap& ta, const CUtensorMap& tb, GemmArgs g,
   return e == cudaSuccess ? ARC_OK : ARC_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------------------------------------
+// Mixture-of-experts drivers
+// ---------------------------------------------------------------------------------------------
+
+arc_status expert_dims(int64_t tokens, int32_t k, int32_t experts) {
+  if (tokens <= 0 || k <= 0 || experts <= 0) return ARC_ERR_INVALID_ARG;
+  if (k > 1024 || experts > arc::kMaxExperts || tokens > (1ll << 28) / k) return ARC_ERR_UNSUPPORTED;
+  return ARC_OK;
+}
+
+int64_t expert_max_blocks(int64_t slots, int32_t experts) {
+  return (slots + 127 * std::min<int64_t>(experts, slots)) / 128;
+}
+
+// A launch that may begin while the kernel before it ends (every kernel launched here waits for
+// that kernel before it touches memory), of clusters of `cluster` CTAs.
+template <typename... P, typename... A>
+arc_status launch_pdl(void (*kern)(P...), int64_t grid, int block, size_t smem, int cluster, cudaStream_t s, A... args) {
+  if (grid > 0x7FFFFFFF) return ARC_ERR_UNSUPPORTED;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess) return ARC_OK;
+  (void)cudaGetLastError();  // reported here, not by a later call
+  return ARC_ERR_CUDA;
+}
+
+// CTAs of the move kernels: a warp per (token, segment of 32 u vectors).
+int64_t move_blocks(int64_t tokens, int64_t vecs, int u) {
+  const int64_t tasks = tokens * ((vecs + 32 * u - 1) / (32 * u));
+  return (tasks + arc::kMoveThreads / 32 - 1) / (arc::kMoveThreads / 32);
+}
+
+arc_status move_check(int64_t d, int64_t ld_a, int64_t ld_b, const void* a, const void* b, const int32_t* plan,
+                      int64_t tokens, int32_t k, int32_t experts) {
+  if (!a || !b || !plan) return ARC_ERR_INVALID_ARG;
+  const arc_status st = expert_dims(tokens, k, experts);
+  if (st != ARC_OK) return st;
+  if (d <= 0 || d % 8 || ld_a < d || ld_b < d || ld_a % 8 || ld_b % 8) return ARC_ERR_INVALID_ARG;
+  if (d > (1ll << 24)) return ARC_ERR_UNSUPPORTED;
+  if (!al16(a) || !al16(b) || !al16(plan)) return ARC_ERR_ALIGNMENT;
+  return ARC_OK;
+}
+
+template <int SRC>
+arc_status quantize_experts(const void* x, int64_t ldx, int64_t K, const int32_t* idx, int32_t r, const int32_t* plan,
+                            int64_t tokens, int32_t k, int32_t experts, uint8_t* codes, uint8_t* sf,
+                            arc_stream_t stream) {
+  if (!x || !plan || !codes || !sf) return ARC_ERR_INVALID_ARG;
+  arc_status st = expert_dims(tokens, k, experts);
+  if (st != ARC_OK) return st;
+  const int64_t width = SRC == arc::kQexSwiglu ? 2 * K : K;
+  if (K <= 0 || K % 32 || r < 0 || r % 32 || r > K || ldx < width || (r > 0 && !idx)) return ARC_ERR_INVALID_ARG;
+  if (K > (1ll << 20) || r > 32767) return ARC_ERR_UNSUPPORTED;
+  if (!al16(x) || (ldx * 2) % 16 || !al16(plan) || !al16(codes) || !al16(sf)) return ARC_ERR_ALIGNMENT;
+  st = device_check(nullptr);
+  if (st != ARC_OK) return st;
+  arc::QuantExpertsArgs a;
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.ldx = ldx;
+  a.n = SRC == arc::kQexTokens ? tokens : tokens * k;
+  a.K = static_cast<int>(K);
+  a.r = r;
+  a.kpad = static_cast<int>(arc_kpad(K + r));
+  a.katoms = (a.kpad + 127) / 128;
+  a.idx = idx;
+  a.p = arc::plan_sections(plan, tokens * k, experts);
+  a.k = k;
+  a.experts = experts;
+  a.codes = codes;
+  a.sf = sf;
+  const int64_t tasks = a.n * ((K / 32 + 15) / 16 + r / 32);
+  return launch_pdl(arc::k_quant_experts<SRC>, (tasks + 7) / 8, 256, 0, 1, S(stream), a);
+}
+
+template <int KIND, int CG>
+arc_status expert_gemm_launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
+                              arc::ExpertGemmArgs g, int64_t slots, int sms, cudaStream_t s) {
+  using T = arc::ExpertGemmTraits<KIND, CG>;
+  // the most tiles that the routing can make; the kernel reads the real number from the plan
+  const int64_t max_m = (slots + static_cast<int64_t>(T::TM - 1) * std::min<int64_t>(g.experts, slots)) / T::TM;
+  const int64_t units = std::min<int64_t>(max_m * g.tiles_n, sms / CG);
+  // row tiles whose A rows, about 36 MB, stay in L2 while a column block streams by (as gemm_launch)
+  const int64_t a_row_bytes = static_cast<int64_t>(g.ksteps) * (T::MX4 ? 34 : 32);
+  g.group_m = static_cast<int>(std::max<int64_t>(1, (36ll << 20) / (T::TM * a_row_bytes)));
+  return launch_pdl(arc::k_gemm_experts<KIND, CG>, units * CG, arc::kGemmThreads,
+                    arc::expert_gemm_smem_bytes<KIND, CG>(g.experts), CG, s, ta, tb, ty, g);
+}
+
+template <int KIND>
+arc_status expert_gemm(const void* a, int64_t a_pitch, const uint8_t* a_sf, const void* b, int64_t b_pitch,
+                       const uint8_t* b_sf, const int32_t* plan, int64_t tokens, int32_t k, int32_t experts, int64_t N,
+                       int64_t K, void* y, int64_t ldy, arc_stream_t stream) {
+  constexpr bool MX4 = KIND == arc::kGemmMX4;
+  int sms = 0;
+  arc_status st = device_check(&sms);
+  if (st != ARC_OK) return st;
+  const int64_t slots = tokens * k;
+  arc::ExpertGemmArgs g;
+  std::memset(&g, 0, sizeof(g));
+  g.p = arc::plan_sections(plan, slots, experts);
+  g.experts = experts;
+  g.N = static_cast<int>(N);
+  g.kstages = static_cast<int>(MX4 ? (K / 64 + 3) / 4 : (K + 63) / 64);
+  g.ksteps = static_cast<int>(MX4 ? K / 64 : 4 * g.kstages);
+  g.katoms = static_cast<int>((K + 127) / 128);
+  g.nblk128 = static_cast<int>((N + 127) / 128);
+  g.tiles_n = static_cast<int>((N + 255) / 256);
+  g.sfa = a_sf;
+  g.sfb = b_sf;
+  g.y = static_cast<__nv_bfloat16*>(y);
+  g.ldy = ldy;
+  g.wait_ns = g_wait_ns;
+  const bool pair = slots >= 128ll * experts;
+  g.box_rows_a = static_cast<int>(std::min<int64_t>(128, slots));
+  g.box_rows_b = static_cast<int>(std::min<int64_t>(pair ? 128 : 256, experts * N));
+  const CUtensorMapDataType dt = MX4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t inner = static_cast<uint64_t>(MX4 ? K / 2 : K);
+  const uint32_t box = MX4 ? 128 : 64;
+  CUtensorMap ta, tb, ty;
+  if (!make_map(&ta, dt, a, inner, static_cast<uint64_t>(slots), static_cast<uint64_t>(a_pitch), box, g.box_rows_a) ||
+      !make_map(&tb, dt, b, inner, static_cast<uint64_t>(experts * N), static_cast<uint64_t>(b_pitch), box,
+                g.box_rows_b) ||
+      !make_store_map(&ty, y, static_cast<uint64_t>(N), static_cast<uint64_t>(slots), static_cast<uint64_t>(ldy) * 2))
+    return ARC_ERR_CUDA;
+  g.inject = take_inject(1);
+  return pair ? expert_gemm_launch<KIND, 2>(ta, tb, ty, g, slots, sms, S(stream))
+              : expert_gemm_launch<KIND, 1>(ta, tb, ty, g, slots, sms, S(stream));
+}
+
 }  // namespace
 
 // =============================================================================================
@@ -586,6 +740,157 @@ arc_status arc_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_sf, const uin
     return ARC_ERR_CUDA;
   g.inject = take_inject(1);
   return gemm_launch<arc::kGemmMX4>(ta, tb, g, sms, add_bf16 != nullptr, S(stream));
+}
+
+size_t arc_expert_plan_bytes(int64_t tokens, int32_t k, int32_t experts) {
+  if (expert_dims(tokens, k, experts) != ARC_OK) return 0;
+  return static_cast<size_t>(2 * arc::plan_pad(experts + 1) + 3 * arc::plan_pad(tokens * k)) * 4;
+}
+
+size_t arc_expert_sf_bytes(int64_t tokens, int32_t k, int32_t experts, int64_t k_aug) {
+  if (expert_dims(tokens, k, experts) != ARC_OK || k_aug <= 0) return 0;
+  return static_cast<size_t>(expert_max_blocks(tokens * k, experts)) *
+         static_cast<size_t>((arc_kpad(k_aug) + 127) / 128) * 512u;
+}
+
+arc_status arc_expert_plan(const void* ids, int32_t id_bytes, int64_t ld_ids, int64_t tokens, int32_t k,
+                           int32_t experts, int32_t* plan, size_t plan_bytes, arc_stream_t stream) {
+  if (!ids || !plan) return ARC_ERR_INVALID_ARG;
+  arc_status st = expert_dims(tokens, k, experts);
+  if (st != ARC_OK) return st;
+  if ((id_bytes != 4 && id_bytes != 8) || ld_ids < k) return ARC_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(ids) & static_cast<uintptr_t>(id_bytes - 1)) || !al16(plan)) return ARC_ERR_ALIGNMENT;
+  if (plan_bytes < arc_expert_plan_bytes(tokens, k, experts)) return ARC_ERR_WORKSPACE;
+  st = device_check(nullptr);
+  if (st != ARC_OK) return st;
+  const int slots = static_cast<int>(tokens * k);
+  const int ctas = slots > 4096 ? arc::kPlanMaxCtas : 1;
+  const size_t smem = arc::plan_smem_bytes(experts);
+  return id_bytes == 4 ? launch_pdl(arc::k_expert_plan<int32_t>, ctas, arc::kPlanThreads, smem, ctas, S(stream),
+                                    static_cast<const int32_t*>(ids), ld_ids, slots, k, experts, plan)
+                       : launch_pdl(arc::k_expert_plan<int64_t>, ctas, arc::kPlanThreads, smem, ctas, S(stream),
+                                    static_cast<const int64_t*>(ids), ld_ids, slots, k, experts, plan);
+}
+
+arc_status arc_dispatch_experts_bf16(const void* x_bf16, int64_t ldx, int64_t d, const int32_t* plan, int64_t tokens,
+                                     int32_t k, int32_t experts, void* rows_bf16, int64_t ld_rows,
+                                     arc_stream_t stream) {
+  arc_status st = move_check(d, ldx, ld_rows, x_bf16, rows_bf16, plan, tokens, k, experts);
+  if (st != ARC_OK) return st;
+  if ((st = device_check(nullptr)) != ARC_OK) return st;
+  return launch_pdl(arc::k_dispatch<1>, move_blocks(tokens, d / 8, 1), arc::kMoveThreads, 0, 1, S(stream),
+                    static_cast<const __nv_bfloat16*>(x_bf16), ldx, static_cast<int>(d / 8),
+                    arc::plan_sections(plan, tokens * k, experts), tokens, k, static_cast<__nv_bfloat16*>(rows_bf16),
+                    ld_rows);
+}
+
+static arc_status combine_rows(const void* rows, int64_t ld_rows, int64_t d, const float* weights, int64_t ld_weights,
+                               const int32_t* plan, int64_t tokens, int32_t k, int32_t experts, const void* add,
+                               int64_t ld_add, void* y, int64_t ldy, arc_stream_t stream) {
+  arc_status st = device_check(nullptr);
+  if (st != ARC_OK) return st;
+  return launch_pdl(arc::k_combine<1>, move_blocks(tokens, d / 8, 1), arc::kMoveThreads, 0, 1, S(stream),
+                    static_cast<const __nv_bfloat16*>(rows), ld_rows, static_cast<int>(d / 8), weights, ld_weights,
+                    arc::plan_sections(plan, tokens * k, experts), tokens, k, static_cast<const __nv_bfloat16*>(add),
+                    ld_add, static_cast<__nv_bfloat16*>(y), ldy);
+}
+
+arc_status arc_dispatch_experts_grad_bf16(const void* d_rows_bf16, int64_t ld_rows, int64_t d, const int32_t* plan,
+                                          int64_t tokens, int32_t k, int32_t experts, void* d_x_bf16, int64_t ldx,
+                                          arc_stream_t stream) {
+  const arc_status st = move_check(d, ldx, ld_rows, d_x_bf16, d_rows_bf16, plan, tokens, k, experts);
+  if (st != ARC_OK) return st;
+  return combine_rows(d_rows_bf16, ld_rows, d, nullptr, 0, plan, tokens, k, experts, nullptr, 0, d_x_bf16, ldx,
+                      stream);
+}
+
+arc_status arc_combine_experts_bf16(const void* rows_bf16, int64_t ld_rows, int64_t d, const float* weights,
+                                    int64_t ld_weights, const int32_t* plan, int64_t tokens, int32_t k,
+                                    int32_t experts, const void* add_bf16, int64_t ld_add, void* y_bf16, int64_t ldy,
+                                    arc_stream_t stream) {
+  const arc_status st = move_check(d, ldy, ld_rows, y_bf16, rows_bf16, plan, tokens, k, experts);
+  if (st != ARC_OK) return st;
+  if (!weights || ld_weights < k || (add_bf16 && (ld_add < d || ld_add % 8))) return ARC_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(weights) & 3u) || (add_bf16 && !al16(add_bf16))) return ARC_ERR_ALIGNMENT;
+  return combine_rows(rows_bf16, ld_rows, d, weights, ld_weights, plan, tokens, k, experts, add_bf16, ld_add, y_bf16,
+                      ldy, stream);
+}
+
+arc_status arc_combine_experts_grad_bf16(const void* d_y_bf16, int64_t ld_dy, const void* rows_bf16, int64_t ld_rows,
+                                         int64_t d, const float* weights, int64_t ld_weights, const int32_t* plan,
+                                         int64_t tokens, int32_t k, int32_t experts, void* d_rows_bf16,
+                                         int64_t ld_drows, float* d_weights, int64_t ld_dw, arc_stream_t stream) {
+  arc_status st = move_check(d, ld_dy, ld_rows, d_y_bf16, rows_bf16, plan, tokens, k, experts);
+  if (st != ARC_OK) return st;
+  if (!weights || !d_weights || !d_rows_bf16 || ld_weights < k || ld_dw < k || ld_drows < d || ld_drows % 8)
+    return ARC_ERR_INVALID_ARG;
+  if (!al16(d_rows_bf16) || ((reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(d_weights)) & 3u))
+    return ARC_ERR_ALIGNMENT;
+  if ((st = device_check(nullptr)) != ARC_OK) return st;
+  const int64_t slots = tokens * k;
+  return launch_pdl(arc::k_combine_grad, (slots + arc::kMoveThreads / 32 - 1) / (arc::kMoveThreads / 32),
+                    arc::kMoveThreads, 0, 1, S(stream), static_cast<const __nv_bfloat16*>(d_y_bf16), ld_dy,
+                    static_cast<const __nv_bfloat16*>(rows_bf16), ld_rows, static_cast<int>(d / 8), weights,
+                    ld_weights, arc::plan_sections(plan, slots, experts), tokens, k,
+                    static_cast<__nv_bfloat16*>(d_rows_bf16), ld_drows, d_weights, ld_dw);
+}
+
+arc_status arc_quantize_act_experts_mxfp4(const void* x_bf16, int64_t ldx, int64_t K, const int32_t* d_idx, int32_t r,
+                                          const int32_t* plan, int64_t tokens, int32_t k, int32_t experts,
+                                          uint8_t* codes, uint8_t* sf, arc_stream_t stream) {
+  return quantize_experts<arc::kQexTokens>(x_bf16, ldx, K, d_idx, r, plan, tokens, k, experts, codes, sf, stream);
+}
+
+arc_status arc_quantize_swiglu_experts_mxfp4(const void* gu_bf16, int64_t ld_gu, int64_t F, const int32_t* d_idx,
+                                             int32_t r, const int32_t* plan, int64_t tokens, int32_t k,
+                                             int32_t experts, uint8_t* codes, uint8_t* sf, arc_stream_t stream) {
+  return quantize_experts<arc::kQexSwiglu>(gu_bf16, ld_gu, F, d_idx, r, plan, tokens, k, experts, codes, sf, stream);
+}
+
+arc_status arc_pack_weight_experts_mxfp4(const void* w_bf16, int32_t experts, int64_t N, int64_t K, int64_t ldw,
+                                         const int32_t* d_idx, int32_t r, uint8_t* codes, uint8_t* sf,
+                                         arc_stream_t stream) {
+  if (experts <= 0 || N <= 0) return ARC_ERR_INVALID_ARG;
+  if (experts > arc::kMaxExperts || N > (1ll << 30) / experts) return ARC_ERR_UNSUPPORTED;
+  // scale blocks begin anew with every expert: whole blocks are one matrix, others go one by one
+  if (N % 128 == 0) return quantize_mx(w_bf16, experts * N, K, ldw, d_idx, r, codes, sf, stream, 1);
+  for (int32_t e = 0; e < experts; ++e) {
+    const arc_status st = quantize_mx(w_bf16 ? static_cast<const uint16_t*>(w_bf16) + e * N * ldw : nullptr, N, K, ldw,
+                                      d_idx, r, codes ? codes + e * arc_nvfp4_codes_bytes(N, K + r) : nullptr,
+                                      sf ? sf + e * arc_mxfp4_sf_bytes(N, K + r) : nullptr, stream, 1);
+    if (st != ARC_OK) return st;
+  }
+  return ARC_OK;
+}
+
+arc_status arc_gemm_experts_mxfp4(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* b_codes,
+                                  const uint8_t* b_sf, const int32_t* plan, int64_t tokens, int32_t k,
+                                  int32_t experts, int64_t N, int64_t k_aug, void* y_bf16, int64_t ldy,
+                                  arc_stream_t stream) {
+  if (!a_codes || !a_sf || !b_codes || !b_sf || !plan || !y_bf16) return ARC_ERR_INVALID_ARG;
+  const arc_status st = expert_dims(tokens, k, experts);
+  if (st != ARC_OK) return st;
+  if (N <= 0 || k_aug <= 0 || N % 8 || ldy < N || ldy % 8) return ARC_ERR_INVALID_ARG;
+  if (N > (1ll << 30) / experts || k_aug > (1ll << 24)) return ARC_ERR_UNSUPPORTED;
+  if (!al16(a_codes) || !al16(a_sf) || !al16(b_codes) || !al16(b_sf) || !al16(plan) || !al16(y_bf16))
+    return ARC_ERR_ALIGNMENT;
+  const int64_t kpad = arc_kpad(k_aug);
+  return expert_gemm<arc::kGemmMX4>(a_codes, kpad / 2, a_sf, b_codes, kpad / 2, b_sf, plan, tokens, k, experts, N,
+                                    kpad, y_bf16, ldy, stream);
+}
+
+arc_status arc_gemm_experts_bf16(const void* rows_bf16, int64_t ld_rows, const void* w_bf16, int64_t ldw,
+                                 const int32_t* plan, int64_t tokens, int32_t k, int32_t experts, int64_t N,
+                                 int64_t K, void* y_bf16, int64_t ldy, arc_stream_t stream) {
+  if (!rows_bf16 || !w_bf16 || !plan || !y_bf16) return ARC_ERR_INVALID_ARG;
+  const arc_status st = expert_dims(tokens, k, experts);
+  if (st != ARC_OK) return st;
+  if (N <= 0 || K <= 0 || K % 8 || N % 8 || ld_rows < K || ldw < K || ldy < N || ld_rows % 8 || ldw % 8 || ldy % 8)
+    return ARC_ERR_INVALID_ARG;
+  if (N > (1ll << 30) / experts || K > (1ll << 24)) return ARC_ERR_UNSUPPORTED;
+  if (!al16(rows_bf16) || !al16(w_bf16) || !al16(plan) || !al16(y_bf16)) return ARC_ERR_ALIGNMENT;
+  return expert_gemm<arc::kGemmBF16>(rows_bf16, ld_rows * 2, nullptr, w_bf16, ldw * 2, nullptr, plan, tokens, k,
+                                     experts, N, K, y_bf16, ldy, stream);
 }
 
 arc_status arc_gemm_bf16(const void* x_bf16, int64_t ldx, const void* w_bf16, int64_t ldw, int64_t M, int64_t N,
