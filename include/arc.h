@@ -306,17 +306,18 @@ arc_status arc_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_sf, const uin
  *   sf_row      [S]      the row's place in the scale layout, 128 * blocks[e] + row - offsets[e];
  *                        -1 behind the last row in use
  *
- * MXFP4 operands in sorted order: codes [S, K_pad/2] by sorted row; scale bytes in the 512-byte
- * atoms of arc_quantize_act_mxfp4, but by sf_row, so that every expert begins a new 128-row block
- * (arc_expert_sf_bytes bytes). Scale bytes of places that no row has are left as they were.
+ * MXFP4 operands in sorted order: codes [S, K_pad/2] by sorted row. Scale byte kb (channels 32 kb
+ * ..) of the row at place m = sf_row lies at ((kb / 8) * R + m) * 8 + kb % 8, with R = 128 *
+ * floor((S + 127 * min(E, S)) / 128) places: 8 bytes per row for each 256 channels (one stage of the
+ * product), every expert beginning a new block of 128 places. Bytes of places that no row has, and
+ * behind K_pad / 32 columns, are left as they were.
  * Packed weights of E experts: codes [E * N, K_pad/2]; scale bytes of expert e at
  * e * arc_mxfp4_sf_bytes(N, K + r).
  *
- * Limits of every call of this section: 1 <= E <= 1024, 1 <= k <= 1024, 1 <= T, S <= 2^28.
+ * Limits of every call of this section: 1 <= E <= 512, 1 <= k <= 1024, 1 <= T, S <= 2^28.
  */
 size_t arc_expert_plan_bytes(int64_t tokens, int32_t k, int32_t experts);
-/* Bytes of the scale layout of S sorted rows of k_aug channels: (the most 128-row blocks that S
- * slots of E experts can take, floor((S + 127 * min(E, S)) / 128)) * ceil(K_pad/128) * 512. */
+/* Bytes of the scale layout of S sorted rows of k_aug channels: ceil(K_pad/256) * R * 8. */
 size_t arc_expert_sf_bytes(int64_t tokens, int32_t k, int32_t experts, int64_t k_aug);
 
 /*

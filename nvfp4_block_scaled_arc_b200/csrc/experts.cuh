@@ -4,8 +4,8 @@
 //
 // Slot s = token * k + choice; offsets[e] is the first sorted row of expert e, blocks[e] its first
 // 128-row block of scale bytes. Sorted rows are dense (no padding between experts), so everything
-// here moves only rows that exist; the scale bytes alone begin a new 128-row block per expert,
-// because the block-scaled GEMM reads them by 128-row atoms.
+// here moves only rows that exist; the scale bytes alone begin a new 128-row block per expert, so
+// that a tile's scale bytes always begin on the 16-byte boundary that a bulk copy needs.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -14,7 +14,7 @@
 
 namespace arc {
 
-constexpr int kMaxExperts = 1024;
+constexpr int kMaxExperts = 512;
 
 // Sections of the plan, each beginning at a multiple of 64 values.
 __host__ __device__ constexpr int64_t plan_pad(int64_t n) { return (n + 63) / 64 * 64; }
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
       if (c < cta) before += v;
     }
   }
-  // exclusive scan over the experts (E <= 1024: one thread each)
+  // exclusive scan over the experts (E <= 1024 threads: one each)
   const int nblk = (total + 127) >> 7;
   int rows_in = total, blocks_in = nblk;
 #pragma unroll
@@ -343,8 +343,9 @@ constexpr int kQexTokens = 0, kQexSwiglu = 1;
 struct QuantExpertsArgs {
   const __nv_bfloat16* x;  // tokens [T, K], or gate|up [S, 2 K]
   int64_t ldx;
-  int64_t n;               // tokens, or slots
-  int K, r, kpad, katoms;  // katoms = ceil(K_pad / 128)
+  int64_t n;        // tokens, or slots
+  int K, r, kpad;
+  int64_t sf_rows;  // rows of the scale layout
   const int32_t* idx;
   Plan p;
   int k, experts;
@@ -398,7 +399,8 @@ __global__ void __launch_bounds__(256) k_quant_experts(QuantExpertsArgs a) {
       if (dst >= 0) sfr = a.p.sf_row[dst];
     }
   };
-  auto sf_base = [&](int64_t m) { return a.sf + (m >> 7) * a.katoms * 512 + (m & 31) * 16 + ((m >> 5) & 3) * 4; };
+  // scale byte kb of place m: 8 bytes (a K = 256 pipeline stage of the product) per row and stage
+  auto sf_at = [&](int64_t m, int kb) { return a.sf + ((kb >> 3) * a.sf_rows + m) * 8 + (kb & 7); };
   int dst0, sfr0;
   places(0, dst0, sfr0);
   if (part < nseg) {
@@ -414,9 +416,14 @@ __global__ void __launch_bounds__(256) k_quant_experts(QuantExpertsArgs a) {
     for (int e = 0; e < 8; ++e) p[e] = f2_pack(bf16_lo(w[e]), bf16_hi(w[e]));
     uint2 cc = mx_encode16(p, mx_inv_scale(sb));
     if (am == 0u) cc = make_uint2(0u, 0u);
-    // the last segment also zeroes the columns behind the appended blocks
-    const int ncols = 4 * a.katoms, pad0 = nblk + nres;
-    const bool last = part == nseg - 1;
+    // four lane pairs' scale bytes make one 32-bit word, in lanes 0, 8, 16, 24
+    uint32_t sw = sb;
+    sw |= __shfl_down_sync(0xFFFFFFFFu, sw, 2) << 8;
+    sw |= __shfl_down_sync(0xFFFFFFFFu, sw, 4) << 16;
+    const bool whole = (b & ~3) + 3 < nblk;  // the word's four blocks exist
+    // the last segment also zeroes the block that pads an odd number of blocks to K_pad
+    const int kbz = nblk + nres;
+    const bool pad = part == nseg - 1 && 32 * kbz < a.kpad;
     for (int j0 = 0; j0 < nrows; j0 += 32) {
       if (j0) places(j0, dst0, sfr0);
       const int nj = min(32, nrows - j0);
@@ -425,15 +432,15 @@ __global__ void __launch_bounds__(256) k_quant_experts(QuantExpertsArgs a) {
         const int64_t m = __shfl_sync(0xFFFFFFFFu, sfr0, j);
         if (dst < 0) continue;
         uint8_t* crow = a.codes + dst * cpitch;
-        uint8_t* srow = sf_base(m);
-        if (b < nblk) {
-          *reinterpret_cast<uint2*>(crow + 16 * b + 8 * half) = cc;
-          if (!half) srow[(b >> 2) * 512 + (b & 3)] = static_cast<uint8_t>(sb);
+        if (b < nblk) *reinterpret_cast<uint2*>(crow + 16 * b + 8 * half) = cc;
+        if (whole) {
+          if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(sf_at(m, b)) = sw;
+        } else if (b < nblk && !half) {
+          *sf_at(m, b) = static_cast<uint8_t>(sb);
         }
-        if (last && pad0 + lane < ncols) {
-          const int kb = pad0 + lane;
-          if (16 * kb < cpitch) *reinterpret_cast<uint4*>(crow + 16 * kb) = make_uint4(0, 0, 0, 0);
-          srow[(kb >> 2) * 512 + (kb & 3)] = 0;
+        if (pad && lane == 0) {
+          *reinterpret_cast<uint4*>(crow + 16 * kbz) = make_uint4(0, 0, 0, 0);
+          *sf_at(m, kbz) = 0;
         }
       }
     }
@@ -479,7 +486,7 @@ __global__ void __launch_bounds__(256) k_quant_experts(QuantExpertsArgs a) {
         if (dst < 0) continue;
         if ((lane & 7) == 0)
           *reinterpret_cast<uint32_t*>(a.codes + dst * cpitch + 16 * kb + (lane >> 1)) = code;
-        if (lane == 1) sf_base(m)[(kb >> 2) * 512 + (kb & 3)] = static_cast<uint8_t>(sb);
+        if (lane == 1) *sf_at(m, kb) = static_cast<uint8_t>(sb);
       }
     }
   }

@@ -70,14 +70,10 @@ arc_status device_check(int* sms) {
                              arc::gemm_smem_bytes<arc::kGemmMX4>()) != cudaSuccess ||
         cudaFuncSetAttribute(arc::k_gemm<arc::kGemmMX4, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              arc::gemm_smem_bytes<arc::kGemmMX4>()) != cudaSuccess ||
-        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             arc::expert_gemm_smem_bytes<arc::kGemmMX4, 1>(arc::kMaxExperts)) != cudaSuccess ||
-        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             arc::expert_gemm_smem_bytes<arc::kGemmMX4, 2>(arc::kMaxExperts)) != cudaSuccess ||
-        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmBF16, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             arc::expert_gemm_smem_bytes<arc::kGemmBF16, 1>(arc::kMaxExperts)) != cudaSuccess ||
-        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmBF16, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             arc::expert_gemm_smem_bytes<arc::kGemmBF16, 2>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmMX4>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmBF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmBF16>(arc::kMaxExperts)) != cudaSuccess ||
         cudaFuncSetAttribute(arc::k_expert_plan<int32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(arc::plan_smem_bytes(arc::kMaxExperts))) != cudaSuccess ||
         cudaFuncSetAttribute(arc::k_expert_plan<int64_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -131,14 +127,15 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Y [outer, inner] bf16, row pitch in bytes, as the target of 32-row x 16-column TMA stores
-// (no swizzle; the staging chunk is 32 rows of 32 bytes).
-bool make_store_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_bytes) {
+// Y [outer, inner] bf16, row pitch in bytes, as the target of TMA stores (no swizzle; the staging
+// chunk is box_outer rows of box_inner values).
+bool make_store_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_bytes,
+                    uint32_t box_inner = 16, uint32_t box_outer = 32) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {pitch_bytes};
-  cuuint32_t box[2] = {16, 32};
+  cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
@@ -449,7 +446,7 @@ arc_status quantize_experts(const void* x, int64_t ldx, int64_t K, const int32_t
   a.K = static_cast<int>(K);
   a.r = r;
   a.kpad = static_cast<int>(arc_kpad(K + r));
-  a.katoms = (a.kpad + 127) / 128;
+  a.sf_rows = 128 * expert_max_blocks(tokens * k, experts);
   a.idx = idx;
   a.p = arc::plan_sections(plan, tokens * k, experts);
   a.k = k;
@@ -460,25 +457,12 @@ arc_status quantize_experts(const void* x, int64_t ldx, int64_t K, const int32_t
   return launch_pdl(arc::k_quant_experts<SRC>, (tasks + 7) / 8, 256, 0, 1, S(stream), a);
 }
 
-template <int KIND, int CG>
-arc_status expert_gemm_launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ty,
-                              arc::ExpertGemmArgs g, int64_t slots, int sms, cudaStream_t s) {
-  using T = arc::ExpertGemmTraits<KIND, CG>;
-  // the most tiles that the routing can make; the kernel reads the real number from the plan
-  const int64_t max_m = (slots + static_cast<int64_t>(T::TM - 1) * std::min<int64_t>(g.experts, slots)) / T::TM;
-  const int64_t units = std::min<int64_t>(max_m * g.tiles_n, sms / CG);
-  // row tiles whose A rows, about 36 MB, stay in L2 while a column block streams by (as gemm_launch)
-  const int64_t a_row_bytes = static_cast<int64_t>(g.ksteps) * (T::MX4 ? 34 : 32);
-  g.group_m = static_cast<int>(std::max<int64_t>(1, (36ll << 20) / (T::TM * a_row_bytes)));
-  return launch_pdl(arc::k_gemm_experts<KIND, CG>, units * CG, arc::kGemmThreads,
-                    arc::expert_gemm_smem_bytes<KIND, CG>(g.experts), CG, s, ta, tb, ty, g);
-}
-
 template <int KIND>
 arc_status expert_gemm(const void* a, int64_t a_pitch, const uint8_t* a_sf, const void* b, int64_t b_pitch,
                        const uint8_t* b_sf, const int32_t* plan, int64_t tokens, int32_t k, int32_t experts, int64_t N,
                        int64_t K, void* y, int64_t ldy, arc_stream_t stream) {
-  constexpr bool MX4 = KIND == arc::kGemmMX4;
+  using T = arc::ExpertGemmTraits<KIND>;
+  constexpr bool MX4 = T::MX4;
   int sms = 0;
   arc_status st = device_check(&sms);
   if (st != ARC_OK) return st;
@@ -492,27 +476,35 @@ arc_status expert_gemm(const void* a, int64_t a_pitch, const uint8_t* a_sf, cons
   g.ksteps = static_cast<int>(MX4 ? K / 64 : 4 * g.kstages);
   g.katoms = static_cast<int>((K + 127) / 128);
   g.nblk128 = static_cast<int>((N + 127) / 128);
-  g.tiles_n = static_cast<int>((N + 255) / 256);
-  g.sfa = a_sf;
-  g.sfb = b_sf;
+  g.tiles_w = static_cast<int>((N + T::TM - 1) / T::TM);
+  // row tiles whose rows, about 36 MB, stay in L2 while the weights stream by (as gemm_launch)
+  g.group_m = static_cast<int>(std::max<int64_t>(1, (36ll << 20) / (T::TN * static_cast<int64_t>(g.ksteps) * (MX4 ? 34 : 32))));
+  g.box_w = static_cast<int>(std::min<int64_t>(T::BM, experts * N));
+  g.sfx_rows = 128 * expert_max_blocks(slots, experts);
+  g.sfx = a_sf;
+  g.sfw = b_sf;
   g.y = static_cast<__nv_bfloat16*>(y);
   g.ldy = ldy;
+  g.slots = slots;
   g.wait_ns = g_wait_ns;
-  const bool pair = slots >= 128ll * experts;
-  g.box_rows_a = static_cast<int>(std::min<int64_t>(128, slots));
-  g.box_rows_b = static_cast<int>(std::min<int64_t>(pair ? 128 : 256, experts * N));
   const CUtensorMapDataType dt = MX4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t inner = static_cast<uint64_t>(MX4 ? K / 2 : K);
   const uint32_t box = MX4 ? 128 : 64;
-  CUtensorMap ta, tb, ty;
-  if (!make_map(&ta, dt, a, inner, static_cast<uint64_t>(slots), static_cast<uint64_t>(a_pitch), box, g.box_rows_a) ||
-      !make_map(&tb, dt, b, inner, static_cast<uint64_t>(experts * N), static_cast<uint64_t>(b_pitch), box,
-                g.box_rows_b) ||
-      !make_store_map(&ty, y, static_cast<uint64_t>(N), static_cast<uint64_t>(slots), static_cast<uint64_t>(ldy) * 2))
+  CUtensorMap tw, ty;
+  arc::ExpertRowMaps tx;
+  if (!make_map(&tw, dt, b, inner, static_cast<uint64_t>(experts * N), static_cast<uint64_t>(b_pitch), box, g.box_w) ||
+      !make_store_map(&ty, y, static_cast<uint64_t>(N), static_cast<uint64_t>(slots), static_cast<uint64_t>(ldy) * 2,
+                      32, 16))
     return ARC_ERR_CUDA;
+  for (int i = 0; i < arc::kRowBoxes; ++i)
+    if (!make_map(&tx.box[i], dt, a, inner, static_cast<uint64_t>(slots), static_cast<uint64_t>(a_pitch), box,
+                  static_cast<uint32_t>(std::min<int64_t>(8 << i, slots))))
+      return ARC_ERR_CUDA;
+  // the most tiles that the routing can make; the kernel reads the real number from the plan
+  const int64_t max_tiles = (slots + (T::TN - 1) * std::min<int64_t>(experts, slots)) / T::TN * g.tiles_w;
   g.inject = take_inject(1);
-  return pair ? expert_gemm_launch<KIND, 2>(ta, tb, ty, g, slots, sms, S(stream))
-              : expert_gemm_launch<KIND, 1>(ta, tb, ty, g, slots, sms, S(stream));
+  return launch_pdl(arc::k_gemm_experts<KIND>, 2 * std::min<int64_t>(max_tiles, sms / 2), arc::kGemmThreads,
+                    arc::expert_gemm_smem_bytes<KIND>(experts), 2, S(stream), tw, tx, ty, g);
 }
 
 }  // namespace
@@ -749,8 +741,8 @@ size_t arc_expert_plan_bytes(int64_t tokens, int32_t k, int32_t experts) {
 
 size_t arc_expert_sf_bytes(int64_t tokens, int32_t k, int32_t experts, int64_t k_aug) {
   if (expert_dims(tokens, k, experts) != ARC_OK || k_aug <= 0) return 0;
-  return static_cast<size_t>(expert_max_blocks(tokens * k, experts)) *
-         static_cast<size_t>((arc_kpad(k_aug) + 127) / 128) * 512u;
+  return static_cast<size_t>(expert_max_blocks(tokens * k, experts)) * 128u *
+         static_cast<size_t>((arc_kpad(k_aug) + 255) / 256) * 8u;
 }
 
 arc_status arc_expert_plan(const void* ids, int32_t id_bytes, int64_t ld_ids, int64_t tokens, int32_t k,

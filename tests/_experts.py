@@ -50,9 +50,13 @@ def f64(t: torch.Tensor) -> np.ndarray:
     return t.detach().double().cpu().numpy()
 
 
-def sf_canonical(sf: np.ndarray, sf_row: np.ndarray, ncols: int) -> np.ndarray:
-    """Scale bytes [rows, ncols] of the rows at places sf_row of the 512-byte atoms."""
-    atoms = (ncols + 3) // 4
+def sf_places(slots: int, experts: int) -> int:
+    """Places of the scale layout."""
+    return (slots + 127 * min(experts, slots)) // 128 * 128
+
+
+def sf_canonical(sf: np.ndarray, sf_row: np.ndarray, ncols: int, places: int) -> np.ndarray:
+    """Scale bytes [rows, ncols] of the rows at places sf_row."""
     m = sf_row[:, None].astype(np.int64)
     kb = np.arange(ncols)[None, :]
-    return sf[(m // 128 * atoms + kb // 4) * 512 + m % 32 * 16 + m // 32 % 4 * 4 + kb % 4]
+    return sf[(kb // 8 * places + m) * 8 + kb % 8]

@@ -13,7 +13,7 @@ import torch
 import nvfp4_block_scaled_arc_b200 as arc
 import oracle as O
 import workloads as W
-from tests._experts import bf16, f64, make_ids, plan_of, sf_canonical
+from tests._experts import bf16, f64, make_ids, plan_of, sf_canonical, sf_places
 from tests._helpers import to_bits, to_dev
 
 pytestmark = pytest.mark.gpu
@@ -35,7 +35,7 @@ def _status_ok():
 
 @pytest.mark.parametrize("tokens,k,experts,how", [
     (1, 1, 1, "skewed"), (1, 8, 128, "skewed"), (3, 2, 5, "drop"), (130, 3, 7, "drop"), (257, 4, 256, "skewed"),
-    (1000, 8, 1024, "skewed"), (513, 8, 16, "one"), (4099, 6, 61, "drop"), (16384, 8, 64, "skewed"),
+    (1000, 8, 512, "skewed"), (513, 8, 16, "one"), (4099, 6, 61, "drop"), (16384, 8, 64, "skewed"),
     (2, 1024, 33, "repeat"), (5000, 1, 3, "repeat")])
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 def test_plan_is_the_stable_sort(tokens, k, experts, how, dtype):
@@ -205,15 +205,15 @@ def _check_coded(q, p, codes_ref, sc_ref, k_aug):
     codes = q.codes.view(-1, kp // 2).cpu().numpy()
     np.testing.assert_array_equal(codes[:used], codes_ref)
     assert (codes[used:] == 0xA5).all()
-    ncols = (kp + 127) // 128 * 4
-    got = sf_canonical(q.sf.cpu().numpy(), p["sf_row"][:used], ncols)
+    sf, ncols = q.sf.cpu().numpy(), (kp + 255) // 256 * 8
+    places = sf_places(len(p["slot_of_row"]), len(p["offsets"]) - 1)
+    assert sf.size == places * ncols
+    got = sf_canonical(sf, p["sf_row"][:used], ncols, places)
     np.testing.assert_array_equal(got[:, : kp // 32], sc_ref)
-    assert (got[:, kp // 32:] == 0).all()
-    # places without a row are left as they were
-    touched = np.zeros(q.sf.numel() // 512 // (ncols // 4) * 128, bool)
-    touched[p["sf_row"][:used]] = True
-    rest = np.flatnonzero(~touched)
-    assert (sf_canonical(q.sf.cpu().numpy(), rest, ncols) == 0xA5).all()
+    # columns behind K_pad and places without a row are left as they were
+    assert (got[:, kp // 32:] == 0xA5).all()
+    rest = np.setdiff1d(np.arange(places), p["sf_row"][:used])
+    assert (sf_canonical(sf, rest, ncols, places) == 0xA5).all()
 
 
 def _coded_out(plan, k_aug):
