@@ -106,6 +106,16 @@ __device__ __forceinline__ void mbar_arrive_cta(uint64_t* bar, uint32_t rank) {
       "r"(rank)
       : "memory");
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
                "r"(ncols)
@@ -275,60 +285,62 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   auto tile = [&](int t) { return expert_tile(t, first, offsets, g.experts, g.tiles_w, g.group_m); };
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------------ producer
-      uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
-      bool skip = (g.inject == 1) && blockIdx.x == 0;
-      bool ok = true;
-      for (int t = unit; t < ntiles && ok; t += units) {
-        const ExpertTile at = tile(t);
-        const int w_row = at.e * g.N + at.tw * T::TM + static_cast<int>(rank) * T::BM;
-        const int x_row = offsets[at.e] + at.row + static_cast<int>(rank) * (at.n >> 1);
-        int bi = 0;  // the smallest box of 8 << bi rows that holds the CTA's half
-        while ((8 << bi) < (at.n >> 1)) ++bi;
-        const int box_x = static_cast<int>(min(static_cast<int64_t>(8 << bi), g.slots));
-        const bool has_sfw = MX4 && 2 * at.tw + static_cast<int>(rank) < g.nblk128;
-        const int64_t sf0 = MX4 ? 128ll * g.p.blocks[at.e] + at.row : 0;
-        for (int ks = 0; ks < g.kstages; ++ks) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, g.wait_ns, abort_flag)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sW = smem + stage * T::STAGE_BYTES;
-          uint8_t* sX = sW + T::W_BYTES;
-          if (skip) {
-            skip = false;  // failure injection: this stage's loads are never issued
-          } else {
-            uint32_t bytes = static_cast<uint32_t>(g.box_w + box_x) * 128u;
-            if (MX4) {
-              bytes += static_cast<uint32_t>(at.n) * 8u;
-              if (has_sfw) bytes += static_cast<uint32_t>(min(2, g.katoms - 2 * ks)) * 512u;
-            }
+    // -------------------------------------------------------------------- producer
+    uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
+    bool skip = (g.inject == 1) && blockIdx.x == 0;
+    bool ok = true;
+    for (int t = unit; t < ntiles && ok; t += units) {
+      const ExpertTile at = tile(t);
+      const int w_row = at.e * g.N + at.tw * T::TM + static_cast<int>(rank) * T::BM;
+      const int x_row = offsets[at.e] + at.row + static_cast<int>(rank) * (at.n >> 1);
+      int bi = 0;  // the smallest box of 8 << bi rows that holds the CTA's half
+      while ((8 << bi) < (at.n >> 1)) ++bi;
+      const int box_x = static_cast<int>(min(static_cast<int64_t>(8 << bi), g.slots));
+      const CUtensorMap* map_x = &tmX.box[bi];
+      const bool has_sfw = MX4 && 2 * at.tw + static_cast<int>(rank) < g.nblk128;
+      const uint8_t* sfx = MX4 ? g.sfx + (128ll * g.p.blocks[at.e] + at.row) * 8 : nullptr;
+      const uint32_t bytes0 = static_cast<uint32_t>(g.box_w + box_x) * 128u + (MX4 ? static_cast<uint32_t>(at.n) * 8u : 0u);
+      for (int ks = 0; ks < g.kstages; ++ks) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], phase ^ 1u, g.wait_ns, abort_flag))) {
+          ok = false;
+          break;
+        }
+        if (skip) {
+          skip = false;  // failure injection: this stage's loads are never issued
+        } else {
+          if (elect_one()) {
+            uint8_t* sW = smem + stage * T::STAGE_BYTES;
+            uint8_t* sX = sW + T::W_BYTES;
+            uint32_t bytes = bytes0;
+            if (has_sfw) bytes += static_cast<uint32_t>(min(2, g.katoms - 2 * ks)) * 512u;
             mbar_arrive_expect_tx(&full[stage], bytes);
             const int kx = MX4 ? ks * 128 : ks * 64;
             tma_load_2d(sW, &tmW, &full[stage], kx, w_row);
-            tma_load_2d(sX, &tmX.box[bi], &full[stage], kx, x_row);
+            tma_load_2d(sX, map_x, &full[stage], kx, x_row);
             if (MX4)
-              bulk_load(sX + T::X_BYTES + T::SFW_BYTES, g.sfx + (ks * g.sfx_rows + sf0) * 8,
-                        static_cast<uint32_t>(at.n) * 8u, &full[stage]);
-            armed |= 1u << stage;
-            armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+              bulk_load(sX + T::X_BYTES + T::SFW_BYTES, sfx, static_cast<uint32_t>(at.n) * 8u, &full[stage]);
           }
-          if (++stage == T::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          __syncwarp();
+          armed |= 1u << stage;
+          armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+        }
+        sfx += g.sfx_rows * 8;
+        if (++stage == T::STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (*abort_flag) {
-        // let every load this thread issued land before the CTA goes away
-        for (int s = 0; s < T::STAGES; ++s)
-          if ((armed >> s) & 1u) mbar_wait_teardown(&full[s], (armed_par >> s) & 1u, g.wait_ns);
-      }
+    }
+    if (*abort_flag) {
+      // let every load of this warp land before the CTA goes away
+      for (int s = 0; s < T::STAGES; ++s)
+        if ((armed >> s) & 1u) mbar_wait_teardown(&full[s], (armed_par >> s) & 1u, g.wait_ns);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      // ------------------------------------------------------------------ MMA issue (as k_gemm)
+    if (rank == 0) {
+      // ------------------------------------------------------------------ MMA issue
+      // The whole warp walks the stages and one elected lane issues: control flow and operands
+      // stay warp-uniform.
       uint32_t acc = 0, acc_phase = 0, stage = 0, phase = 0;
       bool ok = true;
       constexpr uint64_t kStageDesc = static_cast<uint64_t>(T::STAGE_BYTES >> 4);
@@ -338,11 +350,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       uint32_t sf = tmem + T::SF_COL0;
       for (int t = unit; t < ntiles && ok; t += units) {
         const uint32_t idesc = T::IDESC0 | (static_cast<uint32_t>(tile(t).n >> 3) << 17);
-        if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u, g.wait_ns, abort_flag)) break;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_empty[acc], acc_phase ^ 1u, g.wait_ns, abort_flag))) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem + acc * T::TN;
         for (int ks = 0; ks < g.kstages; ++ks) {
-          if (!mbar_wait(&ready[stage], phase, g.wait_ns, abort_flag)) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ready[stage], phase, g.wait_ns, abort_flag))) {
             ok = false;
             break;
           }
@@ -350,15 +362,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint64_t dx = dw + kXDesc;
           const uint32_t acc0 = ks > 0 ? 1u : 0u;
           const int nk = MX4 ? min(4, g.ksteps - 4 * ks) : 4;
-          if (nk == 4) {
+          if (elect_one()) {
+            if (nk == 4) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              expert_mma<KIND>(d_tmem, dw + 2 * k, dx + 2 * k, idesc, sf, k, k > 0 ? 1u : acc0);
-          } else {
-            for (int k = 0; k < nk; ++k)
-              expert_mma<KIND>(d_tmem, dw + 2 * k, dx + 2 * k, idesc, sf, k, k > 0 ? 1u : acc0);
+              for (int k = 0; k < 4; ++k)
+                expert_mma<KIND>(d_tmem, dw + 2 * k, dx + 2 * k, idesc, sf, k, k > 0 ? 1u : acc0);
+            } else {
+              for (int k = 0; k < nk; ++k)
+                expert_mma<KIND>(d_tmem, dw + 2 * k, dx + 2 * k, idesc, sf, k, k > 0 ? 1u : acc0);
+            }
+            tc_commit_pair(&empty[stage]);
+            if (ks == g.kstages - 1) tc_commit_pair(&acc_full[acc]);
           }
-          tc_commit_pair(&empty[stage]);
+          __syncwarp();
           if (++stage == T::STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -369,53 +385,58 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             sf += T::SF_SET_COLS;
           }
         }
-        if (!ok) break;
-        tc_commit_pair(&acc_full[acc]);
         if (++acc == T::ACC_STAGES) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
       // nothing issued may still be running when the tensor memory is released
-      tc_commit_own(drain);
-      mbar_wait_teardown(drain, 0, g.wait_ns);
+      if (elect_one()) {
+        tc_commit_own(drain);
+        mbar_wait_teardown(drain, 0, g.wait_ns);
+      }
+      __syncwarp();
     }
   } else if (warp == 2) {
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
-      bool ok = true;
-      for (int t = unit; t < ntiles && ok; t += units) {
-        int64_t blk = 0;
-        bool has = false;
-        if (MX4) {
-          const ExpertTile at = tile(t);
-          has = 2 * at.tw + static_cast<int>(rank) < g.nblk128;
-          blk = static_cast<int64_t>(at.e) * g.nblk128 + 2 * at.tw + rank;
+    // -------------------------------------------------------------------- weight scales, or relay
+    uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
+    bool ok = true;
+    for (int t = unit; t < ntiles && ok; t += units) {
+      int64_t blk = 0;
+      bool has = false;
+      if (MX4) {
+        const ExpertTile at = tile(t);
+        has = 2 * at.tw + static_cast<int>(rank) < g.nblk128;
+        blk = static_cast<int64_t>(at.e) * g.nblk128 + 2 * at.tw + rank;
+      }
+      const uint8_t* sfw = MX4 ? g.sfw + blk * g.katoms * 512 : nullptr;
+      for (int ks = 0; ks < g.kstages; ++ks) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(MX4 ? &empty[stage] : &full[stage], MX4 ? phase ^ 1u : phase, g.wait_ns,
+                                               abort_flag))) {
+          ok = false;
+          break;
         }
-        for (int ks = 0; ks < g.kstages; ++ks) {
-          if (!mbar_wait(MX4 ? &empty[stage] : &full[stage], MX4 ? phase ^ 1u : phase, g.wait_ns, abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (!MX4) {
+        if (elect_one()) {
+          if (!MX4)
             mbar_arrive_cta(&ready[stage], 0);  // the relay
-          } else if (has) {
-            // the weights' scale atoms of the stage, beside the producer's copies
-            bulk_load(smem + stage * T::STAGE_BYTES + T::W_BYTES + T::X_BYTES, g.sfw + (blk * g.katoms + 2 * ks) * 512,
+          else if (has)  // the weights' scale atoms of the stage, beside the producer's copies
+            bulk_load(smem + stage * T::STAGE_BYTES + T::W_BYTES + T::X_BYTES, sfw + 1024 * ks,
                       static_cast<uint32_t>(min(2, g.katoms - 2 * ks)) * 512u, &full[stage]);
-            armed |= 1u << stage;
-            armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
-          }
-          if (++stage == T::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (has) {
+          armed |= 1u << stage;
+          armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+        }
+        if (++stage == T::STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (*abort_flag) {
-        for (int s = 0; s < T::STAGES; ++s)
-          if ((armed >> s) & 1u) mbar_wait_teardown(&full[s], (armed_par >> s) & 1u, g.wait_ns);
-      }
+    }
+    if (*abort_flag) {
+      for (int s = 0; s < T::STAGES; ++s)
+        if ((armed >> s) & 1u) mbar_wait_teardown(&full[s], (armed_par >> s) & 1u, g.wait_ns);
     }
   } else if (warp < kGemmEpiWarp0) {
     if (MX4) {
