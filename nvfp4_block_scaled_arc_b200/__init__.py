@@ -596,105 +596,113 @@ class ExpertWeightMXFP4:
     k_aug: int
 
 
-def _raw_stream(device: torch.device, stream) -> int:
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+_current_raw_stream = torch._C._cuda_getCurrentRawStream  # the handle alone; building a Stream object costs 1 us
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _refuse(fn: str, name: str, t: torch.Tensor, dtype, dev: int, shape):
+    if not t.is_cuda:
+        raise ValueError(f"{fn}: tensors must be CUDA tensors ({name} is on {t.device})")
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on cuda:{dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{fn}: {name} must be {list(shape)}, not {list(t.shape)}")
+    raise ValueError(f"{fn}: {name} must hold consecutive values")
+
+
+def _rows_of(fn: str, name: str, t: torch.Tensor, dtype, dev: int, shape: tuple) -> int:
+    """The leading dimension of a [rows, cols] argument; refuses one of another device, dtype, shape
+    or with strided rows. A single row has the row's length, whatever its stride says."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or (t.stride(1) != 1 and shape[1] != 1):
+        _refuse(fn, name, t, dtype, dev, shape)
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _flat(fn: str, name: str, t: torch.Tensor, dtype, dev: int, least: int):
+    """Refuses a buffer of another device or dtype, with gaps, or with fewer than `least` values."""
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(fn, name, t, dtype, dev, None)
+    if t.numel() < least:
+        raise ValueError(f"{fn}: {name} holds {t.numel()} values, {least} are needed")
 
 
 class _on:
     """The device of a call's tensors as the current one, and the caller's stream (if one is given)
-    as the one that its outputs are allocated for."""
+    as the one that its outputs are allocated for. Yields the stream's handle."""
 
-    __slots__ = ("ctx",)
+    __slots__ = ("ctx", "raw")
 
-    def __init__(self, device: torch.device, stream):
+    def __init__(self, fn: str, dev: int, stream):
+        if dev < 0:
+            raise ValueError(f"{fn}: tensors must be CUDA tensors")
         if stream is not None:
-            self.ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
+            if stream.device.index != dev:
+                raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on cuda:{dev}")
+            self.ctx, self.raw = torch.cuda.stream(stream), stream.cuda_stream
         else:
-            self.ctx = None
+            self.ctx = None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+            self.raw = _current_raw_stream(dev)
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
+        return self.raw
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
 
 
-def _expert_args(fn: str, device: torch.device, stream, **tensors):
-    """Refuses tensors (name = (tensor, dtype, shape or None)) that are not what fn takes: on the
-    call's device, of the dtype and shape, with consecutive values in a row."""
-    if device.type != "cuda":
-        raise ValueError(f"{fn}: tensors must be CUDA tensors")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {device}")
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        if t.device != device:
-            raise ValueError(f"{fn}: {name} is on {t.device}, not on {device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{fn}: {name} must be {list(shape)}, not {list(t.shape)}")
-        if t.stride(-1) != 1:
-            raise ValueError(f"{fn}: {name}'s rows must hold consecutive values")
-
-
-def _ld(t: torch.Tensor) -> int:
-    """Leading dimension of [rows, cols]; a single row has the row's length, whatever its stride."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
 def expert_plan(ids: torch.Tensor, experts: int, out: ExpertPlan | None = None, stream=None) -> ExpertPlan:
     """arc_expert_plan: the slots of expert ids [T, k] (int32 or int64) sorted by expert; ids outside
     [0, experts) give their slots no row."""
-    dev = ids.device
-    if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 2:
+    fn, dev, dtype = "expert_plan", ids.get_device(), ids.dtype
+    if (dtype is not torch.int32 and dtype is not torch.int64) or ids.dim() != 2:
         raise ValueError("expert_plan: ids must be [tokens, k] of int32 or int64")
-    _expert_args("expert_plan", dev, stream, ids=(ids, ids.dtype, None),
-                 out=(None if out is None else out.buf, torch.int32, None))
-    T, k = ids.shape
-    with _on(dev, stream):
+    shape = ids.shape
+    T, k = shape
+    with _on(fn, dev, stream) as raw:
+        ld = _rows_of(fn, "ids", ids, dtype, dev, shape)
         if out is None:
             n = 2 * _pad64(experts + 1) + 3 * _pad64(T * k)
-            out = ExpertPlan(torch.empty(n, dtype=torch.int32, device=dev), T, k, experts)
+            out = ExpertPlan(torch.empty(n, dtype=_I32, device=ids.device), T, k, experts)
         elif (out.tokens, out.k, out.experts) != (T, k, experts):
             raise ValueError("expert_plan: out was made for other sizes")
+        buf = out.buf
+        _flat(fn, "out", buf, _I32, dev, 0)
         _check("arc_expert_plan", lib().arc_expert_plan(
-            ids.data_ptr(), ids.element_size(), _ld(ids), T, k, experts, out.buf.data_ptr(), out.buf.numel() * 4,
-            _raw_stream(dev, stream)))
+            ids.data_ptr(), 4 if dtype is torch.int32 else 8, ld, T, k, experts, buf.data_ptr(), buf.numel() * 4, raw))
     return out
 
 
 def dispatch_experts(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """arc_dispatch_experts_bf16: tokens x [T, d] bf16 copied into sorted order [S, d]."""
-    dev, d = x.device, x.shape[-1]
-    _expert_args("dispatch_experts", dev, stream, x=(x, torch.bfloat16, (plan.tokens, d)),
-                 plan=(plan.buf, torch.int32, None), out=(out, torch.bfloat16, (plan.slots, d)))
-    with _on(dev, stream):
+    fn, dev, d, T, k = "dispatch_experts", x.get_device(), x.shape[-1], plan.tokens, plan.k
+    with _on(fn, dev, stream) as raw:
+        ld = _rows_of(fn, "x", x, _BF16, dev, (T, d))
+        _flat(fn, "plan", plan.buf, _I32, dev, 0)
         if out is None:
-            out = torch.empty(plan.slots, d, dtype=torch.bfloat16, device=dev)
+            out = x.new_empty((T * k, d))
         _check("arc_dispatch_experts_bf16", lib().arc_dispatch_experts_bf16(
-            x.data_ptr(), _ld(x), d, plan.buf.data_ptr(), plan.tokens, plan.k, plan.experts, out.data_ptr(), _ld(out),
-            _raw_stream(dev, stream)))
+            x.data_ptr(), ld, d, plan.buf.data_ptr(), T, k, plan.experts, out.data_ptr(),
+            _rows_of(fn, "out", out, _BF16, dev, (T * k, d)), raw))
     return out
 
 
 def dispatch_experts_grad(d_rows: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None,
                           stream=None) -> torch.Tensor:
     """arc_dispatch_experts_grad_bf16: the tokens' gradient [T, d] from the sorted rows' [S, d]."""
-    dev, d = d_rows.device, d_rows.shape[-1]
-    _expert_args("dispatch_experts_grad", dev, stream, d_rows=(d_rows, torch.bfloat16, (plan.slots, d)),
-                 plan=(plan.buf, torch.int32, None), out=(out, torch.bfloat16, (plan.tokens, d)))
-    with _on(dev, stream):
+    fn, dev, d, T, k = "dispatch_experts_grad", d_rows.get_device(), d_rows.shape[-1], plan.tokens, plan.k
+    with _on(fn, dev, stream) as raw:
+        ld = _rows_of(fn, "d_rows", d_rows, _BF16, dev, (T * k, d))
+        _flat(fn, "plan", plan.buf, _I32, dev, 0)
         if out is None:
-            out = torch.empty(plan.tokens, d, dtype=torch.bfloat16, device=dev)
+            out = d_rows.new_empty((T, d))
         _check("arc_dispatch_experts_grad_bf16", lib().arc_dispatch_experts_grad_bf16(
-            d_rows.data_ptr(), _ld(d_rows), d, plan.buf.data_ptr(), plan.tokens, plan.k, plan.experts, out.data_ptr(),
-            _ld(out), _raw_stream(dev, stream)))
+            d_rows.data_ptr(), ld, d, plan.buf.data_ptr(), T, k, plan.experts, out.data_ptr(),
+            _rows_of(fn, "out", out, _BF16, dev, (T, d)), raw))
     return out
 
 
@@ -702,17 +710,17 @@ def combine_experts(rows: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """arc_combine_experts_bf16: y [T, d] = sum over the token's choices of weights [T, k] (fp32) times
     the sorted rows [S, d] (+ add [T, d])."""
-    dev, d = rows.device, rows.shape[-1]
-    _expert_args("combine_experts", dev, stream, rows=(rows, torch.bfloat16, (plan.slots, d)),
-                 weights=(weights, torch.float32, (plan.tokens, plan.k)), plan=(plan.buf, torch.int32, None),
-                 add=(add, torch.bfloat16, (plan.tokens, d)), out=(out, torch.bfloat16, (plan.tokens, d)))
-    with _on(dev, stream):
+    fn, dev, d, T, k = "combine_experts", rows.get_device(), rows.shape[-1], plan.tokens, plan.k
+    with _on(fn, dev, stream) as raw:
+        ld = _rows_of(fn, "rows", rows, _BF16, dev, (T * k, d))
+        ld_w = _rows_of(fn, "weights", weights, _F32, dev, (T, k))
+        _flat(fn, "plan", plan.buf, _I32, dev, 0)
         if out is None:
-            out = torch.empty(plan.tokens, d, dtype=torch.bfloat16, device=dev)
+            out = rows.new_empty((T, d))
         _check("arc_combine_experts_bf16", lib().arc_combine_experts_bf16(
-            rows.data_ptr(), _ld(rows), d, weights.data_ptr(), _ld(weights), plan.buf.data_ptr(), plan.tokens, plan.k,
-            plan.experts, None if add is None else add.data_ptr(), 0 if add is None else _ld(add), out.data_ptr(),
-            _ld(out), _raw_stream(dev, stream)))
+            rows.data_ptr(), ld, d, weights.data_ptr(), ld_w, plan.buf.data_ptr(), T, k, plan.experts,
+            None if add is None else add.data_ptr(), 0 if add is None else _rows_of(fn, "add", add, _BF16, dev, (T, d)),
+            out.data_ptr(), _rows_of(fn, "out", out, _BF16, dev, (T, d)), raw))
     return out
 
 
@@ -721,48 +729,50 @@ def combine_experts_grad(d_y: torch.Tensor, rows: torch.Tensor, weights: torch.T
                          stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """arc_combine_experts_grad_bf16: (d_rows [S, d] bf16, d_weights [T, k] fp32) from d_y [T, d];
     d_rows may be rows."""
-    dev, d = rows.device, rows.shape[-1]
-    _expert_args("combine_experts_grad", dev, stream, d_y=(d_y, torch.bfloat16, (plan.tokens, d)),
-                 rows=(rows, torch.bfloat16, (plan.slots, d)),
-                 weights=(weights, torch.float32, (plan.tokens, plan.k)), plan=(plan.buf, torch.int32, None),
-                 d_rows=(d_rows, torch.bfloat16, (plan.slots, d)),
-                 d_weights=(d_weights, torch.float32, (plan.tokens, plan.k)))
-    with _on(dev, stream):
+    fn, dev, d, T, k = "combine_experts_grad", rows.get_device(), rows.shape[-1], plan.tokens, plan.k
+    with _on(fn, dev, stream) as raw:
+        ld_dy = _rows_of(fn, "d_y", d_y, _BF16, dev, (T, d))
+        ld = _rows_of(fn, "rows", rows, _BF16, dev, (T * k, d))
+        ld_w = _rows_of(fn, "weights", weights, _F32, dev, (T, k))
+        _flat(fn, "plan", plan.buf, _I32, dev, 0)
         if d_rows is None:
-            d_rows = torch.empty(plan.slots, d, dtype=torch.bfloat16, device=dev)
+            d_rows = rows.new_empty((T * k, d))
         if d_weights is None:
-            d_weights = torch.empty(plan.tokens, plan.k, dtype=torch.float32, device=dev)
+            d_weights = weights.new_empty((T, k))
         _check("arc_combine_experts_grad_bf16", lib().arc_combine_experts_grad_bf16(
-            d_y.data_ptr(), _ld(d_y), rows.data_ptr(), _ld(rows), d, weights.data_ptr(), _ld(weights),
-            plan.buf.data_ptr(), plan.tokens, plan.k, plan.experts, d_rows.data_ptr(), _ld(d_rows),
-            d_weights.data_ptr(), _ld(d_weights), _raw_stream(dev, stream)))
+            d_y.data_ptr(), ld_dy, rows.data_ptr(), ld, d, weights.data_ptr(), ld_w, plan.buf.data_ptr(), T, k,
+            plan.experts, d_rows.data_ptr(), _rows_of(fn, "d_rows", d_rows, _BF16, dev, (T * k, d)),
+            d_weights.data_ptr(), _rows_of(fn, "d_weights", d_weights, _F32, dev, (T, k)), raw))
     return d_rows, d_weights
 
 
-def _expert_mx_out(plan: ExpertPlan, k_aug: int, device) -> ExpertMXFP4:
-    codes = torch.empty(plan.slots, (k_aug + 63) // 64 * 32, dtype=torch.uint8, device=device)
-    sf = torch.empty(lib().arc_expert_sf_bytes(plan.tokens, plan.k, plan.experts, k_aug), dtype=torch.uint8,
-                     device=device)
-    return ExpertMXFP4(codes, sf, plan.slots, k_aug)
+def _expert_sf_bytes(plan: ExpertPlan, k_aug: int) -> int:
+    S = plan.tokens * plan.k
+    return (S + 127 * min(plan.experts, S)) // 128 * 1024 * ((_pad64(k_aug) + 255) // 256)
 
 
 def _expert_quantize(fn: str, x: torch.Tensor, plan: ExpertPlan, K: int, idx, out: ExpertMXFP4 | None, stream,
                      rows: int):
-    dev = x.device
+    dev, S = x.get_device(), plan.tokens * plan.k
     r = 0 if idx is None else idx.numel()
-    _expert_args(fn, dev, stream, x=(x, torch.bfloat16, (rows, x.shape[-1])), plan=(plan.buf, torch.int32, None),
-                 idx=(idx, torch.int32, None), codes=(None if out is None else out.codes, torch.uint8, None),
-                 sf=(None if out is None else out.sf, torch.uint8, None))
-    if out is not None and (out.rows != plan.slots or out.k_aug != K + r or
-                            out.codes.numel() < codes_bytes(plan.slots, K + r) or
-                            out.sf.numel() < lib().arc_expert_sf_bytes(plan.tokens, plan.k, plan.experts, K + r)):
-        raise ValueError(f"{fn}: out was made for other sizes")
-    with _on(dev, stream):
+    kp = _pad64(K + r)
+    with _on(fn, dev, stream) as raw:
+        ld = _rows_of(fn, "x" if rows == plan.tokens else "gu", x, _BF16, dev, (rows, x.shape[-1]))
+        _flat(fn, "plan", plan.buf, _I32, dev, 0)
+        if idx is not None:
+            _flat(fn, "idx", idx, _I32, dev, r)
+        nsf = _expert_sf_bytes(plan, K + r)
         if out is None:
-            out = _expert_mx_out(plan, K + r, dev)
+            out = ExpertMXFP4(torch.empty((S, kp // 2), dtype=_U8, device=x.device),
+                              torch.empty(nsf, dtype=_U8, device=x.device), S, K + r)
+        else:
+            if out.rows != S or out.k_aug != K + r:
+                raise ValueError(f"{fn}: out was made for other sizes")
+            _flat(fn, "out.codes", out.codes, _U8, dev, S * kp // 2)
+            _flat(fn, "out.sf", out.sf, _U8, dev, nsf)
         _check("arc_" + fn, getattr(lib(), "arc_" + fn)(
-            x.data_ptr(), _ld(x), K, None if idx is None else idx.data_ptr(), r, plan.buf.data_ptr(), plan.tokens,
-            plan.k, plan.experts, out.codes.data_ptr(), out.sf.data_ptr(), _raw_stream(dev, stream)))
+            x.data_ptr(), ld, K, None if idx is None else idx.data_ptr(), r, plan.buf.data_ptr(), plan.tokens, plan.k,
+            plan.experts, out.codes.data_ptr(), out.sf.data_ptr(), raw))
     return out
 
 
@@ -781,78 +791,80 @@ def quantize_swiglu_experts_mxfp4(gu: torch.Tensor, plan: ExpertPlan, idx: torch
     return _expert_quantize("quantize_swiglu_experts_mxfp4", gu, plan, gu.shape[-1] // 2, idx, out, stream, plan.slots)
 
 
-def pack_weight_experts_mxfp4(w: torch.Tensor, idx: torch.Tensor | None = None, out: ExpertWeightMXFP4 | None = None,
-                              stream=None) -> ExpertWeightMXFP4:
-    """arc_pack_weight_experts_mxfp4: W [E, N, K] bf16 (experts one after another) -> MXFP4 of
-    [W_e | W_e[:, idx]] for every expert."""
-    dev = w.device
-    if w.dim() != 3:
-        raise ValueError("pack_weight_experts_mxfp4: w must be [experts, N, K]")
-    E, N, K = w.shape
-    r = 0 if idx is None else idx.numel()
-    _expert_args("pack_weight_experts_mxfp4", dev, stream, w=(w, torch.bfloat16, None), idx=(idx, torch.int32, None))
-    ld = _expert_weight_ld("pack_weight_experts_mxfp4", w)
-    cb, sb = E * codes_bytes(N, K + r), E * mxfp4_sf_bytes(N, K + r)
-    if out is not None and ((out.experts, out.n, out.k_aug) != (E, N, K + r) or out.codes.numel() < cb or
-                            out.sf.numel() < sb or out.codes.device != dev or out.sf.device != dev):
-        raise ValueError("pack_weight_experts_mxfp4: out was made for other sizes")
-    with _on(dev, stream):
-        if out is None:
-            out = ExpertWeightMXFP4(torch.empty(E * N, cb // max(E * N, 1), dtype=torch.uint8, device=dev),
-                                    torch.empty(sb, dtype=torch.uint8, device=dev), E, N, K + r)
-        _check("arc_pack_weight_experts_mxfp4", lib().arc_pack_weight_experts_mxfp4(
-            w.data_ptr(), E, N, K, ld, None if idx is None else idx.data_ptr(), r, out.codes.data_ptr(),
-            out.sf.data_ptr(), _raw_stream(dev, stream)))
-    return out
-
-
-def _expert_weight_ld(fn: str, w: torch.Tensor) -> int:
-    E, N, K = w.shape
+def _expert_weight_ld(fn: str, w: torch.Tensor, dev: int, E: int, N: int, K: int) -> int:
+    if w.get_device() != dev or w.dtype is not _BF16 or w.shape != (E, N, K) or (w.stride(2) != 1 and K != 1):
+        _refuse(fn, "w", w, _BF16, dev, (E, N, K))
     ld = w.stride(1) if N > 1 else (w.stride(0) if E > 1 else K)
     if E > 1 and w.stride(0) != N * ld:
         raise ValueError(f"{fn}: the experts' weights must lie one after another")
     return ld
 
 
+def pack_weight_experts_mxfp4(w: torch.Tensor, idx: torch.Tensor | None = None, out: ExpertWeightMXFP4 | None = None,
+                              stream=None) -> ExpertWeightMXFP4:
+    """arc_pack_weight_experts_mxfp4: W [E, N, K] bf16 (experts one after another) -> MXFP4 of
+    [W_e | W_e[:, idx]] for every expert."""
+    fn, dev = "pack_weight_experts_mxfp4", w.get_device()
+    if w.dim() != 3:
+        raise ValueError("pack_weight_experts_mxfp4: w must be [experts, N, K]")
+    E, N, K = w.shape
+    r = 0 if idx is None else idx.numel()
+    with _on(fn, dev, stream) as raw:
+        ld = _expert_weight_ld(fn, w, dev, E, N, K)
+        if idx is not None:
+            _flat(fn, "idx", idx, _I32, dev, r)
+        kp, nsf = _pad64(K + r), E * mxfp4_sf_bytes(N, K + r)
+        if out is None:
+            out = ExpertWeightMXFP4(torch.empty((E * N, kp // 2), dtype=_U8, device=w.device),
+                                    torch.empty(nsf, dtype=_U8, device=w.device), E, N, K + r)
+        else:
+            if (out.experts, out.n, out.k_aug) != (E, N, K + r):
+                raise ValueError("pack_weight_experts_mxfp4: out was made for other sizes")
+            _flat(fn, "out.codes", out.codes, _U8, dev, E * N * kp // 2)
+            _flat(fn, "out.sf", out.sf, _U8, dev, nsf)
+        _check("arc_pack_weight_experts_mxfp4", lib().arc_pack_weight_experts_mxfp4(
+            w.data_ptr(), E, N, K, ld, None if idx is None else idx.data_ptr(), r, out.codes.data_ptr(),
+            out.sf.data_ptr(), raw))
+    return out
+
+
 def gemm_experts_mxfp4(a: ExpertMXFP4, w: ExpertWeightMXFP4, plan: ExpertPlan, out: torch.Tensor | None = None,
                        stream=None) -> torch.Tensor:
     """arc_gemm_experts_mxfp4: Y [S, N] bf16 = each sorted row times its expert's weights."""
-    dev = a.codes.device
-    if a.k_aug != w.k_aug or w.experts != plan.experts or a.rows != plan.slots:
+    fn, dev, S, n, ka = "gemm_experts_mxfp4", a.codes.get_device(), plan.tokens * plan.k, w.n, a.k_aug
+    if ka != w.k_aug or w.experts != plan.experts or a.rows != S:
         raise ValueError("gemm_experts_mxfp4: operands of other sizes than the plan's, or of two depths")
-    if (a.codes.numel() < codes_bytes(a.rows, a.k_aug) or w.codes.numel() < codes_bytes(w.experts * w.n, w.k_aug) or
-            a.sf.numel() < lib().arc_expert_sf_bytes(plan.tokens, plan.k, plan.experts, a.k_aug) or
-            w.sf.numel() < w.experts * mxfp4_sf_bytes(w.n, w.k_aug)):
-        raise ValueError("gemm_experts_mxfp4: an operand's buffer is smaller than its sizes say")
-    _expert_args("gemm_experts_mxfp4", dev, stream, a_codes=(a.codes, torch.uint8, None),
-                 a_sf=(a.sf, torch.uint8, None), w_codes=(w.codes, torch.uint8, None), w_sf=(w.sf, torch.uint8, None),
-                 plan=(plan.buf, torch.int32, None), out=(out, torch.bfloat16, (plan.slots, w.n)))
-    with _on(dev, stream):
+    kp = _pad64(ka)
+    with _on(fn, dev, stream) as raw:
+        _flat(fn, "a.codes", a.codes, _U8, dev, S * kp // 2)
+        _flat(fn, "a.sf", a.sf, _U8, dev, _expert_sf_bytes(plan, ka))
+        _flat(fn, "w.codes", w.codes, _U8, dev, w.experts * n * kp // 2)
+        _flat(fn, "w.sf", w.sf, _U8, dev, w.experts * ((n + 127) // 128) * ((kp + 127) // 128) * 512)
+        _flat(fn, "plan", plan.buf, _I32, dev, 0)
         if out is None:
-            out = torch.empty(plan.slots, w.n, dtype=torch.bfloat16, device=dev)
+            out = torch.empty((S, n), dtype=_BF16, device=a.codes.device)
         _check("arc_gemm_experts_mxfp4", lib().arc_gemm_experts_mxfp4(
             a.codes.data_ptr(), a.sf.data_ptr(), w.codes.data_ptr(), w.sf.data_ptr(), plan.buf.data_ptr(), plan.tokens,
-            plan.k, plan.experts, w.n, a.k_aug, out.data_ptr(), _ld(out), _raw_stream(dev, stream)))
+            plan.k, plan.experts, n, ka, out.data_ptr(), _rows_of(fn, "out", out, _BF16, dev, (S, n)), raw))
     return out
 
 
 def gemm_experts_bf16(rows: torch.Tensor, w: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None,
                       stream=None) -> torch.Tensor:
     """arc_gemm_experts_bf16: Y [S, N] = bf16 of each sorted row [S, K] times its expert's W [E, N, K]."""
-    dev, K = rows.device, rows.shape[-1]
+    fn, dev, S, K = "gemm_experts_bf16", rows.get_device(), plan.tokens * plan.k, rows.shape[-1]
     if w.dim() != 3:
         raise ValueError("gemm_experts_bf16: w must be [experts, N, K]")
     N = w.shape[1]
-    _expert_args("gemm_experts_bf16", dev, stream, rows=(rows, torch.bfloat16, (plan.slots, K)),
-                 w=(w, torch.bfloat16, (plan.experts, N, K)), plan=(plan.buf, torch.int32, None),
-                 out=(out, torch.bfloat16, (plan.slots, N)))
-    ld = _expert_weight_ld("gemm_experts_bf16", w)
-    with _on(dev, stream):
+    with _on(fn, dev, stream) as raw:
+        ld = _rows_of(fn, "rows", rows, _BF16, dev, (S, K))
+        ld_w = _expert_weight_ld(fn, w, dev, plan.experts, N, K)
+        _flat(fn, "plan", plan.buf, _I32, dev, 0)
         if out is None:
-            out = torch.empty(plan.slots, N, dtype=torch.bfloat16, device=dev)
+            out = rows.new_empty((S, N))
         _check("arc_gemm_experts_bf16", lib().arc_gemm_experts_bf16(
-            rows.data_ptr(), _ld(rows), w.data_ptr(), ld, plan.buf.data_ptr(), plan.tokens, plan.k, plan.experts, N, K,
-            out.data_ptr(), _ld(out), _raw_stream(dev, stream)))
+            rows.data_ptr(), ld, w.data_ptr(), ld_w, plan.buf.data_ptr(), plan.tokens, plan.k, plan.experts, N, K,
+            out.data_ptr(), _rows_of(fn, "out", out, _BF16, dev, (S, N)), raw))
     return out
 
 

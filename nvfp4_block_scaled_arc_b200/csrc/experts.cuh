@@ -38,19 +38,25 @@ __host__ __device__ inline Plan plan_sections(const int32_t* p, int64_t slots, i
 }
 
 // ---------------------------------------------------------------------------------------------
-// Plan. One cluster of CTAs (one CTA for few slots), so one launch: every warp owns a contiguous
-// range of slots and counts its ids per expert in shared memory; the CTAs exchange their counts
-// through distributed shared memory; a scan over the experts gives offsets and blocks; then every
-// warp walks its range again, 32 slots at a time, and ranks equal ids of the 32 by lane
-// (match.any), which keeps the order of slots within an expert: no atomics decide a place.
+// Plan, in one launch without a grid-wide wait. The slots are cut into parts, one for each cluster
+// of CTAs. A cluster counts the ids of all slots per expert (4 bytes a slot from L2, spread over
+// its CTAs): those before its part and the others, which gives offsets and the first row of its own
+// slots without waiting for another cluster; its CTAs exchange counts through distributed shared
+// memory. Then every warp walks its share of the part, 32 slots at a time, and ranks equal ids by
+// lane, which keeps the order of slots within an expert: no atomic decides a place. The lanes with
+// an equal id come from one vote per bit of the id. Up to 4096 slots one CTA does all. What bounds
+// the ranking is the scattered writing of slot_of_row and sf_row (a sector per slot and array), so
+// it is spread over up to 128 SMs: PLACEHOLDER us for 65536 slots of 64 experts, 26 us with one
+// cluster.
 // ---------------------------------------------------------------------------------------------
 
-constexpr int kPlanThreads = 1024, kPlanWarps = 32, kPlanMaxCtas = 8;
+constexpr int kPlanThreads = 1024, kPlanWarps = 32, kPlanCtas = 8, kPlanMaxParts = 16;
 
-// Dynamic shared memory: per-warp counts [32][E], the CTA's counts [E], row bases [E], and what
-// turns a row of an expert into its place in the scale layout [E].
+// Dynamic shared memory: the part's counts per warp [32][E] and of the CTA [E], all slots' counts
+// before the part and from it on [2][E], row bases [E], and what turns a row of an expert into its
+// place in the scale layout [E].
 __host__ __device__ constexpr size_t plan_smem_bytes(int experts) {
-  return static_cast<size_t>(kPlanWarps + 3) * static_cast<size_t>(experts) * 4;
+  return static_cast<size_t>(kPlanWarps + 5) * static_cast<size_t>(experts) * 4;
 }
 
 template <typename ID>
@@ -62,38 +68,58 @@ __device__ __forceinline__ int expert_id(const ID* ids, int64_t ld, int k, int s
 
 template <typename ID>
 __global__ void __launch_bounds__(kPlanThreads, 1)
-    k_expert_plan(const ID* __restrict__ ids, int64_t ld, int slots, int k, int experts, int32_t* plan) {
+    k_expert_plan(const ID* __restrict__ ids, int64_t ld, int slots, int k, int experts, int ctas, int32_t* plan) {
   namespace cg = cooperative_groups;
   extern __shared__ int32_t plan_sm[];
   __shared__ int32_t scan_rows[kPlanWarps], scan_blocks[kPlanWarps];
   cg::cluster_group cluster = cg::this_cluster();
   pdl_launch_dependents();
-  int32_t* warp_counts = plan_sm;                     // [32][E]
-  int32_t* counts = plan_sm + kPlanWarps * experts;   // [E]
-  int32_t* base = counts + experts;                   // [E] first row of this CTA's slots of the expert
-  int32_t* sf_shift = base + experts;                 // [E] sf_row - row
+  int32_t* warp_counts = plan_sm;                    // [32][E]
+  int32_t* counts = plan_sm + kPlanWarps * experts;  // [E]
+  int32_t* seen = counts + experts;                  // [2][E]
+  int32_t* base = seen + 2 * experts;                // [E] first row of this CTA's slots of the expert
+  int32_t* sf_shift = base + experts;                // [E] sf_row - row
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
-  for (int i = tid; i < kPlanWarps * experts; i += kPlanThreads) warp_counts[i] = 0;
+  const int cta = static_cast<int>(blockIdx.x) % ctas, part = static_cast<int>(blockIdx.x) / ctas;
+  const int parts = static_cast<int>(gridDim.x) / ctas;
+  for (int i = tid; i < (kPlanWarps + 3) * experts; i += kPlanThreads) warp_counts[i] = 0;
   pdl_wait();  // the ids may come from the kernel before
   __syncthreads();
 
-  const int nwarps = ctas * kPlanWarps;
-  const int chunk = (slots + nwarps * 32 - 1) / (nwarps * 32) * 32;
-  const int64_t lo64 = static_cast<int64_t>(cta * kPlanWarps + warp) * chunk;
-  const int lo = static_cast<int>(lo64 < slots ? lo64 : slots);
-  const int hi = min(slots - lo, chunk) + lo;
+  // this part's slots, a contiguous range of whole strips of 32 for every warp of the cluster
+  const int nwarps = parts * ctas * kPlanWarps;
+  const int64_t chunk = (static_cast<int64_t>(slots) + nwarps * 32 - 1) / (nwarps * 32) * 32;
+  const int part_lo = static_cast<int>(min(static_cast<int64_t>(slots), part * ctas * kPlanWarps * chunk));
+  const int lo = static_cast<int>(min(static_cast<int64_t>(slots), part_lo + (cta * kPlanWarps + warp) * chunk));
+  const int hi = static_cast<int>(min(static_cast<int64_t>(slots), lo + chunk));
   int32_t* mine = warp_counts + warp * experts;
-  for (int s = lo + lane; s < hi; s += 128) {  // four independent loads in flight
+  for (int s0 = lo; s0 < hi; s0 += 128) {  // four independent loads in flight
     int e[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) e[u] = s + 32 * u < hi ? expert_id(ids, ld, k, s + 32 * u, experts) : -1;
+    for (int u = 0; u < 4; ++u) {
+      const int s = s0 + 32 * u + lane;
+      e[u] = s < hi ? expert_id(ids, ld, k, s, experts) : -1;
+    }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (e[u] >= 0) atomicAdd(&mine[e[u]], 1);
   }
+  if (parts > 1) {
+    const int share = (slots + ctas - 1) / ctas;
+    const int all_hi = min(slots, (cta + 1) * share);
+    for (int s0 = cta * share; s0 < all_hi; s0 += 4 * kPlanThreads) {
+      int e[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int s = s0 + kPlanThreads * u + tid;
+        e[u] = s < all_hi ? expert_id(ids, ld, k, s, experts) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (e[u] >= 0) atomicAdd(&seen[(s0 + kPlanThreads * u + tid < part_lo ? 0 : experts) + e[u]], 1);
+    }
+  }
   __syncthreads();
-  int total = 0, before = 0;  // thread e < E: rows of expert e in all CTAs, and in the CTAs before
   if (tid < experts) {
     int run = 0;
 #pragma unroll 8
@@ -103,16 +129,22 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
       run += c;
     }
     counts[tid] = run;
+    if (parts == 1) seen[experts + tid] = run;
   }
   cluster.sync();
+  int total = 0, before = 0;  // thread e < E: rows of expert e, and those of slots before this CTA's
   if (tid < experts) {
-    for (int c = 0; c < ctas; ++c) {
-      const int v = *cluster.map_shared_rank(counts + tid, c);
-      total += v;
-      if (c < cta) before += v;
+#pragma unroll
+    for (int c = 0; c < kPlanCtas; ++c) {
+      if (c < ctas) {
+        const int32_t* there = cluster.map_shared_rank(counts, c);
+        const int own = there[tid], bef = there[experts + tid], aft = there[2 * experts + tid];
+        total += bef + aft;
+        before += bef + (c < cta ? own : 0);
+      }
     }
   }
-  // exclusive scan over the experts (E <= 1024 threads: one each)
+  // exclusive scan over the experts (one thread each)
   const int nblk = (total + 127) >> 7;
   int rows_in = total, blocks_in = nblk;
 #pragma unroll
@@ -147,7 +179,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   if (tid < experts) {
     base[tid] = off + before;
     sf_shift[tid] = 128 * blk - off;
-    if (cta == 0) {
+    if (blockIdx.x == 0) {
       g_offsets[tid] = off;
       g_blocks[tid] = blk;
       if (tid == 0) {
@@ -157,22 +189,38 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     }
   }
   __syncthreads();
-  for (int s0 = lo; s0 < hi; s0 += 32) {
-    const int s = s0 + lane;
-    const int e = s < hi ? expert_id(ids, ld, k, s, experts) : -1;
-    const uint32_t peers = __match_any_sync(0xFFFFFFFFu, e);
-    int row = -1;
-    if (e >= 0) row = base[e] + mine[e] + __popc(peers & ((1u << lane) - 1u));
-    __syncwarp();  // every lane has read its count before the first of each expert moves it on
-    if (e >= 0 && (peers & ((1u << lane) - 1u)) == 0u) mine[e] += __popc(peers);
-    __syncwarp();
-    if (s < hi) g_row_of_slot[s] = row;
-    if (e >= 0) {
-      g_slot_of_row[row] = s;
-      g_sf_row[row] = row + sf_shift[e];
+  const uint32_t before_me = (1u << lane) - 1u;
+  const int bits = 32 - __clz(experts - 1);  // of an id (0 for one expert)
+  for (int s0 = lo; s0 < hi; s0 += 128) {
+    int e[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int s = s0 + 32 * u + lane;
+      e[u] = s < hi ? expert_id(ids, ld, k, s, experts) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int s = s0 + 32 * u + lane;
+      uint32_t peers = __ballot_sync(0xFFFFFFFFu, e[u] >= 0);
+      for (int b = 0; b < bits; ++b) {
+        const bool set = (e[u] >> b) & 1;
+        const uint32_t v = __ballot_sync(0xFFFFFFFFu, set);
+        peers &= set ? v : ~v;
+      }
+      int row = -1;
+      if (e[u] >= 0) row = base[e[u]] + mine[e[u]] + __popc(peers & before_me);
+      __syncwarp();  // every lane has read its count before the first of each expert moves it on
+      if (e[u] >= 0 && (peers & before_me) == 0u) mine[e[u]] += __popc(peers);
+      __syncwarp();
+      if (s < hi) g_row_of_slot[s] = row;
+      if (e[u] >= 0) {
+        g_slot_of_row[row] = s;
+        g_sf_row[row] = row + sf_shift[e[u]];
+      }
     }
   }
-  for (int i = all_rows + cta * kPlanThreads + tid; i < slots; i += ctas * kPlanThreads) {
+  for (int64_t i = all_rows + static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid; i < slots;
+       i += static_cast<int64_t>(gridDim.x) * kPlanThreads) {
     g_slot_of_row[i] = -1;
     g_sf_row[i] = -1;
   }
@@ -331,11 +379,11 @@ __global__ void __launch_bounds__(kMoveThreads)
 // ---------------------------------------------------------------------------------------------
 // MXFP4 quantization into sorted order (format and arithmetic of k_quant_mx_rows). SRC tokens: the
 // row of a token is coded once and written to the token's k sorted rows. SRC SwiGLU: row i of
-// gate|up gives act = bf16(silu(gate) * up) (the arithmetic of k_silu_mul), coded into sorted row
-// i; act never goes to memory. A warp takes one task: 16 blocks of 32 values (lane pairs, as
-// k_quant_mx_rows), or one appended block of 32 outlier channels (a lane each: it forms its
-// channel's primary block's maximum again from the row, at most 64 more bytes from L1/L2 per
-// channel, so no two tasks of a row depend on each other and few tokens still fill the machine).
+// gate|up gives act = bf16(silu(gate) * up), coded into sorted row
+// i; act never goes to memory. A CTA takes one source row, a warp 16 blocks of 32 values at a time
+// (lane pairs, as k_quant_mx_rows; the next 16 blocks' values are requested before these are
+// coded). The row's scale bytes stay in shared memory for the appended blocks of 32 outlier
+// channels, a lane each, whose values are read again (two bytes, or a gate and an up).
 // ---------------------------------------------------------------------------------------------
 
 constexpr int kQexTokens = 0, kQexSwiglu = 1;
@@ -353,45 +401,82 @@ struct QuantExpertsArgs {
   uint8_t* sf;
 };
 
-// silu(g) * u of a bf16 pair each, rounded to bf16 (k_silu_mul's arithmetic).
+// silu(g) * u of a bf16 pair each, rounded to bf16. exp(-g) = 2^h (1 + ln2 l) with h + l =
+// -g log2(e) to twice the precision (log2(e) as the sum of two fp32 values, the product's rounding
+// error by a fused multiply-add), so the approximate 2^h, reciprocal and two products leave about
+// 2^-21 relative before the one rounding to bf16. k_silu_mul's exact quotient would make the kernel
+// arithmetic-bound (162 against PLACEHOLDER us at 8192 x 14336); the two differ by a bf16 step where the value
+// lies that near to a rounding border. Below g = -87.3 the reciprocal is
+// flushed and the result is 0, where |silu(g)| < 1.1e-36.
 __device__ __forceinline__ uint32_t silu_mul_pair(uint32_t g, uint32_t u) {
   const float g0 = bf16_lo(g), g1 = bf16_hi(g);
-  const float s0 = __fdiv_rn(g0, __fadd_rn(1.0f, expf(-g0))), s1 = __fdiv_rn(g1, __fadd_rn(1.0f, expf(-g1)));
-  return pack_bf16x2_rn(__fmul_rn(s0, bf16_lo(u)), __fmul_rn(s1, bf16_hi(u)));
+  const uint64_t g2 = f2_pack(g0, g1);
+  const uint64_t x2 = f2_pack(fminf(fmaxf(g0, -88.0f), 88.0f), fminf(fmaxf(g1, -88.0f), 88.0f));
+  constexpr float kL = 1.44269504088896341f, kLo = static_cast<float>(1.44269504088896341 - static_cast<double>(kL));
+  const uint64_t l2 = f2_pack(-kL, -kL);
+  const uint64_t h2 = f2_mul(x2, l2);
+  float h0, h1;
+  f2_unpack(h2, h0, h1);
+  const uint64_t err2 = f2_fma(x2, l2, f2_pack(-h0, -h1));
+  const uint64_t lo2 = f2_fma(x2, f2_pack(-kLo, -kLo), err2);
+  float e0, e1;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(h0));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(h1));
+  const uint64_t e2 = f2_pack(e0, e1);
+  constexpr float kLn2 = 0.693147180559945309f;
+  float d0, d1;  // 1 + exp(-g)
+  f2_unpack(f2_fma(f2_mul(e2, lo2), f2_pack(kLn2, kLn2), e2), d0, d1);
+  d0 = __fadd_rn(1.0f, d0);
+  d1 = __fadd_rn(1.0f, d1);
+  float r0, r1;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1));
+  float a0, a1;
+  f2_unpack(f2_mul(f2_mul(g2, f2_pack(r0, r1)), f2_pack(bf16_lo(u), bf16_hi(u))), a0, a1);
+  return pack_bf16x2_rn(a0, a1);
 }
 
-// 16 consecutive values of the source row from channel c on, as 8 bf16 pairs.
+// 16 consecutive values of the source row from channel c on (SwiGLU: gate and up).
 template <int SRC>
-__device__ __forceinline__ void load16(const __nv_bfloat16* row, int K, int c, uint32_t (&w)[8]) {
-  const uint4 a = ld_nc_v4_l1(row + c), b = ld_nc_v4_l1(row + c + 8);
-  const uint32_t g[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if constexpr (SRC == kQexSwiglu) {
-    const uint4 ua = ld_nc_v4_l1(row + K + c), ub = ld_nc_v4_l1(row + K + c + 8);
-    const uint32_t u[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = silu_mul_pair(g[i], u[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = g[i];
+struct Raw16 {
+  uint4 g0, g1, u0, u1;
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int K, int c, bool ok) {
+    g0 = g1 = u0 = u1 = make_uint4(0, 0, 0, 0);
+    if (!ok) return;
+    g0 = ld_nc_v4_l1(row + c);
+    g1 = ld_nc_v4_l1(row + c + 8);
+    if constexpr (SRC == kQexSwiglu) {
+      u0 = ld_nc_v4_l1(row + K + c);
+      u1 = ld_nc_v4_l1(row + K + c + 8);
+    }
   }
-}
+  __device__ __forceinline__ void pairs(uint32_t (&w)[8]) const {  // as 8 bf16 pairs
+    const uint32_t g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+    const uint32_t u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = SRC == kQexSwiglu ? silu_mul_pair(g[i], u[i]) : g[i];
+  }
+};
+
+constexpr int kQexMaxWarps = 8;
 
 template <int SRC>
-__global__ void __launch_bounds__(256) k_quant_experts(QuantExpertsArgs a) {
-  pdl_launch_dependents();  // the GEMM that follows may set itself up meanwhile
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts(QuantExpertsArgs a) {
+  extern __shared__ uint8_t qex_sb[];  // the row's scale bytes, kMxZeroBlock for an all-zero block
+  pdl_launch_dependents();             // the GEMM that follows may set itself up meanwhile
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = static_cast<int>(blockDim.x >> 5);
   const int nblk = a.K >> 5, nseg = (nblk + 15) >> 4, nres = a.r >> 5;
-  const int ntask = nseg + nres;
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t src = task / ntask;
-  const int part = static_cast<int>(task - src * ntask);
+  const int64_t src = blockIdx.x;
   pdl_wait();
-  if (src >= a.n) return;
   if (SRC == kQexSwiglu && src >= a.p.offsets[a.experts]) return;
   const __nv_bfloat16* row = a.x + src * a.ldx;
   const int64_t cpitch = a.kpad >> 1;
   const int nrows = SRC == kQexTokens ? a.k : 1;
-  // lane j: sorted row and scale place of the source row's j-th destination
+  const int half = lane & 1;
+  int seg = warp;
+  Raw16<SRC> next;
+  next.load(row, a.K, 32 * (seg * 16 + (lane >> 1)) + 16 * half, seg * 16 + (lane >> 1) < nblk);
+  // lane j: sorted row and scale place of the source row's j-th destination (32 at a time)
   auto places = [&](int j0, int& dst, int& sfr) {
     dst = sfr = -1;
     if (j0 + lane < nrows) {
@@ -403,11 +488,26 @@ __global__ void __launch_bounds__(256) k_quant_experts(QuantExpertsArgs a) {
   auto sf_at = [&](int64_t m, int kb) { return a.sf + ((kb >> 3) * a.sf_rows + m) * 8 + (kb & 7); };
   int dst0, sfr0;
   places(0, dst0, sfr0);
-  if (part < nseg) {
-    const int half = lane & 1;
-    const int b = part * 16 + (lane >> 1);
-    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (b < nblk) load16<SRC>(row, a.K, 32 * b + 16 * half, w);
+  // the values of the warp's first appended block
+  int oc = -1;
+  uint32_t og = 0, ou = 0;
+  auto outlier = [&](int rb) {
+    oc = a.idx[32 * rb + lane];
+    if (static_cast<unsigned>(oc) < static_cast<unsigned>(a.K)) {
+      og = ldg_nc_u16(row + oc);
+      if constexpr (SRC == kQexSwiglu) ou = ldg_nc_u16(row + a.K + oc);
+    } else {
+      oc = -1;
+      if (src == 0) set_status(kStatusInvalidArg);
+    }
+  };
+  if (warp < nres) outlier(warp);
+  for (; seg < nseg; seg += nwarps) {
+    const int b = seg * 16 + (lane >> 1);
+    uint32_t w[8];
+    next.pairs(w);
+    const int bn = b + 16 * nwarps;
+    next.load(row, a.K, 32 * bn + 16 * half, bn < nblk);
     const uint32_t mine = __float_as_uint(absmax16_bf16(w));
     const uint32_t am = max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
     const uint32_t sb = mx_scale_byte(am);
@@ -416,6 +516,7 @@ __global__ void __launch_bounds__(256) k_quant_experts(QuantExpertsArgs a) {
     for (int e = 0; e < 8; ++e) p[e] = f2_pack(bf16_lo(w[e]), bf16_hi(w[e]));
     uint2 cc = mx_encode16(p, mx_inv_scale(sb));
     if (am == 0u) cc = make_uint2(0u, 0u);
+    if (nres > 0 && b < nblk && !half) qex_sb[b] = static_cast<uint8_t>(am == 0u ? kMxZeroBlock : sb);
     // four lane pairs' scale bytes make one 32-bit word, in lanes 0, 8, 16, 24
     uint32_t sw = sb;
     sw |= __shfl_down_sync(0xFFFFFFFFu, sw, 2) << 8;
@@ -423,13 +524,14 @@ __global__ void __launch_bounds__(256) k_quant_experts(QuantExpertsArgs a) {
     const bool whole = (b & ~3) + 3 < nblk;  // the word's four blocks exist
     // the last segment also zeroes the block that pads an odd number of blocks to K_pad
     const int kbz = nblk + nres;
-    const bool pad = part == nseg - 1 && 32 * kbz < a.kpad;
+    const bool pad = seg == nseg - 1 && 32 * kbz < a.kpad;
     for (int j0 = 0; j0 < nrows; j0 += 32) {
-      if (j0) places(j0, dst0, sfr0);
+      int dsts = dst0, sfrs = sfr0;
+      if (j0) places(j0, dsts, sfrs);
       const int nj = min(32, nrows - j0);
       for (int j = 0; j < nj; ++j) {
-        const int64_t dst = __shfl_sync(0xFFFFFFFFu, dst0, j);
-        const int64_t m = __shfl_sync(0xFFFFFFFFu, sfr0, j);
+        const int64_t dst = __shfl_sync(0xFFFFFFFFu, dsts, j);
+        const int64_t m = __shfl_sync(0xFFFFFFFFu, sfrs, j);
         if (dst < 0) continue;
         uint8_t* crow = a.codes + dst * cpitch;
         if (b < nblk) *reinterpret_cast<uint2*>(crow + 16 * b + 8 * half) = cc;
@@ -444,29 +546,22 @@ __global__ void __launch_bounds__(256) k_quant_experts(QuantExpertsArgs a) {
         }
       }
     }
-  } else {
-    const int rb = part - nseg;
-    const int c = a.idx[32 * rb + lane];
+  }
+  if (nres == 0) return;
+  __syncthreads();
+  for (int rb = warp; rb < nres; rb += nwarps) {
+    // ---- outlier channels: x - E2M1(code) * X, the code formed again from x and the block's byte
+    if (rb != warp) outlier(rb);
     float res = 0.0f;
-    if (static_cast<unsigned>(c) < static_cast<unsigned>(a.K)) {
-      uint32_t w[8], w2[8];
-      load16<SRC>(row, a.K, c & ~31, w);
-      load16<SRC>(row, a.K, (c & ~31) + 16, w2);
-      const uint32_t am = max(__float_as_uint(absmax16_bf16(w)), __float_as_uint(absmax16_bf16(w2)));
-      uint32_t pair = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i == ((c & 15) >> 1)) pair = (c & 16) ? w2[i] : w[i];
-      }
-      const float xv = (c & 1) ? bf16_hi(pair) : bf16_lo(pair);
+    if (oc >= 0) {
+      const uint32_t xw = SRC == kQexSwiglu ? silu_mul_pair(og, ou) & 0xFFFFu : og;
+      const float xv = __uint_as_float(xw << 16);
+      const uint32_t t = qex_sb[oc >> 5];
       res = xv;
-      if (am != 0u) {
-        const uint32_t t = mx_scale_byte(am);
+      if (t != kMxZeroBlock) {
         float q[8] = {__fmul_rn(xv, mx_inv_scale(t)), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         res = __fsub_rn(xv, __fmul_rn(e2m1_value(e2m1x8_rn_sat(q) & 15u), mx_scale(t)));
       }
-    } else if (src == 0) {
-      set_status(kStatusInvalidArg);
     }
     const uint32_t am = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(res)));
     const uint32_t sb = mx_scale_byte(am);
@@ -478,11 +573,12 @@ __global__ void __launch_bounds__(256) k_quant_experts(QuantExpertsArgs a) {
     code |= __shfl_down_sync(0xFFFFFFFFu, code, 4) << 16;
     const int kb = nblk + rb;
     for (int j0 = 0; j0 < nrows; j0 += 32) {
-      if (j0) places(j0, dst0, sfr0);
+      int dsts = dst0, sfrs = sfr0;
+      if (j0) places(j0, dsts, sfrs);
       const int nj = min(32, nrows - j0);
       for (int j = 0; j < nj; ++j) {
-        const int64_t dst = __shfl_sync(0xFFFFFFFFu, dst0, j);
-        const int64_t m = __shfl_sync(0xFFFFFFFFu, sfr0, j);
+        const int64_t dst = __shfl_sync(0xFFFFFFFFu, dsts, j);
+        const int64_t m = __shfl_sync(0xFFFFFFFFu, sfrs, j);
         if (dst < 0) continue;
         if ((lane & 7) == 0)
           *reinterpret_cast<uint32_t*>(a.codes + dst * cpitch + 16 * kb + (lane >> 1)) = code;

@@ -55,7 +55,11 @@ struct ExpertGemmTraits {
 };
 
 constexpr int kExpertEpiBytes = 16 * 32 * 2;  // 16 rows of Y x 32 features, one per epilogue warp
-constexpr int kRowBoxes = 5;                  // row maps with boxes of 8, 16, 32, 64 and 128 rows
+// Row maps with boxes of 8, 16, 32, 48 .. 128 rows: a stage copies little more of the tile's rows than
+// it has.
+constexpr int kRowBoxes = 9;
+__host__ __device__ constexpr int row_box_index(int rows) { return rows <= 8 ? 0 : (rows + 15) / 16; }
+__host__ __device__ constexpr int row_box_height(int index) { return index == 0 ? 8 : 16 * index; }
 
 // Shared memory behind the stages: staging, barriers (256 B), first tile and first row of every expert.
 template <int KIND>
@@ -293,9 +297,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const ExpertTile at = tile(t);
       const int w_row = at.e * g.N + at.tw * T::TM + static_cast<int>(rank) * T::BM;
       const int x_row = offsets[at.e] + at.row + static_cast<int>(rank) * (at.n >> 1);
-      int bi = 0;  // the smallest box of 8 << bi rows that holds the CTA's half
-      while ((8 << bi) < (at.n >> 1)) ++bi;
-      const int box_x = static_cast<int>(min(static_cast<int64_t>(8 << bi), g.slots));
+      const int bi = row_box_index(at.n >> 1);  // the smallest box that holds the CTA's half
+      const int box_x = static_cast<int>(min(static_cast<int64_t>(row_box_height(bi)), g.slots));
       const CUtensorMap* map_x = &tmX.box[bi];
       const bool has_sfw = MX4 && 2 * at.tw + static_cast<int>(rank) < g.nblk128;
       const uint8_t* sfx = MX4 ? g.sfx + (128ll * g.p.blocks[at.e] + at.row) * 8 : nullptr;

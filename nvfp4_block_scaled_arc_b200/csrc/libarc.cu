@@ -409,6 +409,10 @@ arc_status launch_pdl(void (*kern)(P...), int64_t grid, int block, size_t smem, 
   return ARC_ERR_CUDA;
 }
 
+// 16-byte vectors per lane of the move kernels: four where that still fills the machine, one where
+// a few tokens are spread over more warps.
+int move_unroll(int64_t tokens, int64_t vecs) { return tokens * ((vecs + 127) / 128) >= 148 * 32 ? 4 : 1; }
+
 // CTAs of the move kernels: a warp per (token, segment of 32 u vectors).
 int64_t move_blocks(int64_t tokens, int64_t vecs, int u) {
   const int64_t tasks = tokens * ((vecs + 32 * u - 1) / (32 * u));
@@ -453,8 +457,12 @@ arc_status quantize_experts(const void* x, int64_t ldx, int64_t K, const int32_t
   a.experts = experts;
   a.codes = codes;
   a.sf = sf;
-  const int64_t tasks = a.n * ((K / 32 + 15) / 16 + r / 32);
-  return launch_pdl(arc::k_quant_experts<SRC>, (tasks + 7) / 8, 256, 0, 1, S(stream), a);
+  // as many warps as the row has segments of 512 values, or as divide them into the fewest rounds
+  const int nseg = static_cast<int>((K / 32 + 15) / 16);
+  const int rounds = (nseg + arc::kQexMaxWarps - 1) / arc::kQexMaxWarps;
+  const int warps = (nseg + rounds - 1) / rounds;
+  return launch_pdl(arc::k_quant_experts<SRC>, a.n, 32 * warps, r > 0 ? static_cast<size_t>(K / 32) : 0, 1, S(stream),
+                    a);
 }
 
 template <int KIND>
@@ -498,7 +506,7 @@ arc_status expert_gemm(const void* a, int64_t a_pitch, const uint8_t* a_sf, cons
     return ARC_ERR_CUDA;
   for (int i = 0; i < arc::kRowBoxes; ++i)
     if (!make_map(&tx.box[i], dt, a, inner, static_cast<uint64_t>(slots), static_cast<uint64_t>(a_pitch), box,
-                  static_cast<uint32_t>(std::min<int64_t>(8 << i, slots))))
+                  static_cast<uint32_t>(std::min<int64_t>(arc::row_box_height(i), slots))))
       return ARC_ERR_CUDA;
   // the most tiles that the routing can make; the kernel reads the real number from the plan
   const int64_t max_tiles = (slots + (T::TN - 1) * std::min<int64_t>(experts, slots)) / T::TN * g.tiles_w;
@@ -756,12 +764,14 @@ arc_status arc_expert_plan(const void* ids, int32_t id_bytes, int64_t ld_ids, in
   st = device_check(nullptr);
   if (st != ARC_OK) return st;
   const int slots = static_cast<int>(tokens * k);
-  const int ctas = slots > 4096 ? arc::kPlanMaxCtas : 1;
+  const int ctas = slots > 4096 ? arc::kPlanCtas : 1;
+  const int parts = std::min(std::max(slots / 4096, 1), arc::kPlanMaxParts);
   const size_t smem = arc::plan_smem_bytes(experts);
-  return id_bytes == 4 ? launch_pdl(arc::k_expert_plan<int32_t>, ctas, arc::kPlanThreads, smem, ctas, S(stream),
-                                    static_cast<const int32_t*>(ids), ld_ids, slots, k, experts, plan)
-                       : launch_pdl(arc::k_expert_plan<int64_t>, ctas, arc::kPlanThreads, smem, ctas, S(stream),
-                                    static_cast<const int64_t*>(ids), ld_ids, slots, k, experts, plan);
+  return id_bytes == 4
+             ? launch_pdl(arc::k_expert_plan<int32_t>, ctas * parts, arc::kPlanThreads, smem, ctas, S(stream),
+                          static_cast<const int32_t*>(ids), ld_ids, slots, k, experts, ctas, plan)
+             : launch_pdl(arc::k_expert_plan<int64_t>, ctas * parts, arc::kPlanThreads, smem, ctas, S(stream),
+                          static_cast<const int64_t*>(ids), ld_ids, slots, k, experts, ctas, plan);
 }
 
 arc_status arc_dispatch_experts_bf16(const void* x_bf16, int64_t ldx, int64_t d, const int32_t* plan, int64_t tokens,
@@ -770,10 +780,11 @@ arc_status arc_dispatch_experts_bf16(const void* x_bf16, int64_t ldx, int64_t d,
   arc_status st = move_check(d, ldx, ld_rows, x_bf16, rows_bf16, plan, tokens, k, experts);
   if (st != ARC_OK) return st;
   if ((st = device_check(nullptr)) != ARC_OK) return st;
-  return launch_pdl(arc::k_dispatch<1>, move_blocks(tokens, d / 8, 1), arc::kMoveThreads, 0, 1, S(stream),
-                    static_cast<const __nv_bfloat16*>(x_bf16), ldx, static_cast<int>(d / 8),
-                    arc::plan_sections(plan, tokens * k, experts), tokens, k, static_cast<__nv_bfloat16*>(rows_bf16),
-                    ld_rows);
+  const int u = move_unroll(tokens, d / 8);
+  return launch_pdl(u == 4 ? arc::k_dispatch<4> : arc::k_dispatch<1>, move_blocks(tokens, d / 8, u),
+                    arc::kMoveThreads, 0, 1, S(stream), static_cast<const __nv_bfloat16*>(x_bf16), ldx,
+                    static_cast<int>(d / 8), arc::plan_sections(plan, tokens * k, experts), tokens, k,
+                    static_cast<__nv_bfloat16*>(rows_bf16), ld_rows);
 }
 
 static arc_status combine_rows(const void* rows, int64_t ld_rows, int64_t d, const float* weights, int64_t ld_weights,
@@ -781,8 +792,9 @@ static arc_status combine_rows(const void* rows, int64_t ld_rows, int64_t d, con
                                int64_t ld_add, void* y, int64_t ldy, arc_stream_t stream) {
   arc_status st = device_check(nullptr);
   if (st != ARC_OK) return st;
-  return launch_pdl(arc::k_combine<1>, move_blocks(tokens, d / 8, 1), arc::kMoveThreads, 0, 1, S(stream),
-                    static_cast<const __nv_bfloat16*>(rows), ld_rows, static_cast<int>(d / 8), weights, ld_weights,
+  const int u = move_unroll(tokens, d / 8);
+  return launch_pdl(u == 4 ? arc::k_combine<4> : arc::k_combine<1>, move_blocks(tokens, d / 8, u),
+                    arc::kMoveThreads, 0, 1, S(stream), static_cast<const __nv_bfloat16*>(rows), ld_rows, static_cast<int>(d / 8), weights, ld_weights,
                     arc::plan_sections(plan, tokens * k, experts), tokens, k, static_cast<const __nv_bfloat16*>(add),
                     ld_add, static_cast<__nv_bfloat16*>(y), ldy);
 }
