@@ -43,14 +43,13 @@ __host__ __device__ inline Plan plan_sections(const int32_t* p, int64_t slots, i
 // its CTAs): those before its part and the others, which gives offsets and the first row of its own
 // slots without waiting for another cluster; its CTAs exchange counts through distributed shared
 // memory. Then every warp walks its share of the part, 32 slots at a time, and ranks equal ids by
-// lane, which keeps the order of slots within an expert: no atomic decides a place. The lanes with
-// an equal id come from one vote per bit of the id. Up to 4096 slots one CTA does all. What bounds
-// the ranking is the scattered writing of slot_of_row and sf_row (a sector per slot and array), so
-// it is spread over up to 128 SMs: PLACEHOLDER us for 65536 slots of 64 experts, 26 us with one
-// cluster.
+// lane (one vote per bit of the id), which keeps the order of slots within an expert: atomics count,
+// none decides a place. Up to 4096 slots one CTA does all. What bounds it is instructions per slot
+// and the latency of a dozen barriers: 3.3 us for 8 slots, 8.6 us for 65536 slots of 64 experts (15.1
+// us with one cluster), 11.2 us for 131072 slots of 256 (28.0 us; 19.7 us in 16 parts).
 // ---------------------------------------------------------------------------------------------
 
-constexpr int kPlanThreads = 1024, kPlanWarps = 32, kPlanCtas = 8, kPlanMaxParts = 16;
+constexpr int kPlanThreads = 1024, kPlanWarps = 32, kPlanCtas = 8, kPlanMaxParts = 8;
 
 // Dynamic shared memory: the part's counts per warp [32][E] and of the CTA [E], all slots' counts
 // before the part and from it on [2][E], row bases [E], and what turns a row of an expert into its
@@ -61,9 +60,24 @@ __host__ __device__ constexpr size_t plan_smem_bytes(int experts) {
 
 template <typename ID>
 __device__ __forceinline__ int expert_id(const ID* ids, int64_t ld, int k, int s, int experts) {
-  const int t = s / k;
-  const ID v = ids[t * ld + (s - t * k)];
+  int64_t at = s;
+  if (ld != k) {  // rows with a stride: the division costs as much as all else
+    const int t = s / k;
+    at = t * ld + (s - t * k);
+  }
+  const ID v = ids[at];
   return v >= 0 && v < experts ? static_cast<int>(v) : -1;
+}
+
+// Lanes of the warp whose expert is this lane's (none has e < 0).
+__device__ __forceinline__ uint32_t same_expert(int e, int bits) {
+  uint32_t peers = __ballot_sync(0xFFFFFFFFu, e >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const bool set = (e >> b) & 1;
+    const uint32_t v = __ballot_sync(0xFFFFFFFFu, set);
+    peers &= set ? v : ~v;
+  }
+  return peers;
 }
 
 template <typename ID>
@@ -82,6 +96,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = static_cast<int>(blockIdx.x) % ctas, part = static_cast<int>(blockIdx.x) / ctas;
   const int parts = static_cast<int>(gridDim.x) / ctas;
+  const uint32_t before_me = (1u << lane) - 1u;
+  const int bits = 32 - __clz(experts - 1);  // of an id (0 for one expert)
   for (int i = tid; i < (kPlanWarps + 3) * experts; i += kPlanThreads) warp_counts[i] = 0;
   pdl_wait();  // the ids may come from the kernel before
   __syncthreads();
@@ -107,16 +123,16 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   if (parts > 1) {
     const int share = (slots + ctas - 1) / ctas;
     const int all_hi = min(slots, (cta + 1) * share);
-    for (int s0 = cta * share; s0 < all_hi; s0 += 4 * kPlanThreads) {
-      int e[4];
+    for (int s0 = cta * share + tid; s0 < all_hi; s0 += 8 * kPlanThreads) {
+      int e[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int s = s0 + kPlanThreads * u + tid;
+      for (int u = 0; u < 8; ++u) {
+        const int s = s0 + kPlanThreads * u;
         e[u] = s < all_hi ? expert_id(ids, ld, k, s, experts) : -1;
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (e[u] >= 0) atomicAdd(&seen[(s0 + kPlanThreads * u + tid < part_lo ? 0 : experts) + e[u]], 1);
+      for (int u = 0; u < 8; ++u)
+        if (e[u] >= 0) atomicAdd(&seen[(s0 + kPlanThreads * u < part_lo ? 0 : experts) + e[u]], 1);
     }
   }
   __syncthreads();
@@ -160,16 +176,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     scan_blocks[warp] = blocks_in;
   }
   __syncthreads();
-  int rows0 = 0, blocks0 = 0, all_rows = 0, all_blocks = 0;
-  for (int w = 0; w < kPlanWarps; ++w) {
-    const int a = scan_rows[w], b = scan_blocks[w];
-    if (w < warp) {
-      rows0 += a;
-      blocks0 += b;
+  // every warp scans the 32 warps' sums
+  int rows_w = scan_rows[lane], blocks_w = scan_blocks[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xFFFFFFFFu, rows_w, o), b = __shfl_up_sync(0xFFFFFFFFu, blocks_w, o);
+    if (lane >= o) {
+      rows_w += a;
+      blocks_w += b;
     }
-    all_rows += a;
-    all_blocks += b;
   }
+  const int all_rows = __shfl_sync(0xFFFFFFFFu, rows_w, 31), all_blocks = __shfl_sync(0xFFFFFFFFu, blocks_w, 31);
+  const int rows0 = __shfl_sync(0xFFFFFFFFu, rows_w, warp) - scan_rows[warp];
+  const int blocks0 = __shfl_sync(0xFFFFFFFFu, blocks_w, warp) - scan_blocks[warp];
   const int off = rows0 + rows_in - total, blk = blocks0 + blocks_in - nblk;
   int32_t* g_offsets = plan;
   int32_t* g_blocks = g_offsets + plan_pad(experts + 1);
@@ -189,8 +208,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     }
   }
   __syncthreads();
-  const uint32_t before_me = (1u << lane) - 1u;
-  const int bits = 32 - __clz(experts - 1);  // of an id (0 for one expert)
   for (int s0 = lo; s0 < hi; s0 += 128) {
     int e[4];
 #pragma unroll
@@ -200,13 +217,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
+      if (s0 + 32 * u >= hi) break;  // the same for the warp
       const int s = s0 + 32 * u + lane;
-      uint32_t peers = __ballot_sync(0xFFFFFFFFu, e[u] >= 0);
-      for (int b = 0; b < bits; ++b) {
-        const bool set = (e[u] >> b) & 1;
-        const uint32_t v = __ballot_sync(0xFFFFFFFFu, set);
-        peers &= set ? v : ~v;
-      }
+      const uint32_t peers = same_expert(e[u], bits);
       int row = -1;
       if (e[u] >= 0) row = base[e[u]] + mine[e[u]] + __popc(peers & before_me);
       __syncwarp();  // every lane has read its count before the first of each expert moves it on

@@ -765,7 +765,7 @@ arc_status arc_expert_plan(const void* ids, int32_t id_bytes, int64_t ld_ids, in
   if (st != ARC_OK) return st;
   const int slots = static_cast<int>(tokens * k);
   const int ctas = slots > 4096 ? arc::kPlanCtas : 1;
-  const int parts = std::min(std::max(slots / 4096, 1), arc::kPlanMaxParts);
+  const int parts = std::min(std::max(slots / 16384, 1), arc::kPlanMaxParts);
   const size_t smem = arc::plan_smem_bytes(experts);
   return id_bytes == 4
              ? launch_pdl(arc::k_expert_plan<int32_t>, ctas * parts, arc::kPlanThreads, smem, ctas, S(stream),
