@@ -393,9 +393,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 // MXFP4 quantization into sorted order (format and arithmetic of k_quant_mx_rows). SRC tokens: the
 // row of a token is coded once and written to the token's k sorted rows. SRC SwiGLU: row i of
 // gate|up gives act = bf16(silu(gate) * up), coded into sorted row
-// i; act never goes to memory. A CTA takes one source row, a warp 16 blocks of 32 values at a time
-// (lane pairs, as k_quant_mx_rows; the next 16 blocks' values are requested before these are
-// coded). The row's scale bytes stay in shared memory for the appended blocks of 32 outlier
+// i; act never goes to memory. A CTA takes one source row, a lane one block of 32 values (one
+// 16-byte store of codes for each destination). The row's scale bytes stay in shared memory for the appended blocks of 32 outlier
 // channels, a lane each, whose values are read again (two bytes, or a gate and an up).
 // ---------------------------------------------------------------------------------------------
 
@@ -414,62 +413,48 @@ struct QuantExpertsArgs {
   uint8_t* sf;
 };
 
-// silu(g) * u of a bf16 pair each, rounded to bf16. exp(-g) = 2^h (1 + ln2 l) with h + l =
-// -g log2(e) to twice the precision (log2(e) as the sum of two fp32 values, the product's rounding
-// error by a fused multiply-add), so the approximate 2^h, reciprocal and two products leave about
-// 2^-21 relative before the one rounding to bf16. k_silu_mul's exact quotient would make the kernel
-// arithmetic-bound (162 against PLACEHOLDER us at 8192 x 14336); the two differ by a bf16 step where the value
-// lies that near to a rounding border. Below g = -87.3 the reciprocal is
-// flushed and the result is 0, where |silu(g)| < 1.1e-36.
+// silu(g) * u of a bf16 pair each, rounded to bf16: 2^(-g log2 e), one added, the reciprocal, two
+// products, in fp32 with the approximate 2^x and reciprocal (2 ulp and 1 ulp). The product -g log2 e is
+// off by half an ulp, a relative |g| 2^-24 of the exponential, so the result is good to about 2^-21
+// for g >= -8 and 2^-18 at g = -60 before its one rounding to bf16 (2^-9); below g = -87.3 the
+// reciprocal is flushed and it is 0, where |silu| < 1.1e-36. k_silu_mul's correctly rounded quotient
+// would bound the kernel by its arithmetic (162 against 110 us at 8192 x 14336).
 __device__ __forceinline__ uint32_t silu_mul_pair(uint32_t g, uint32_t u) {
-  const float g0 = bf16_lo(g), g1 = bf16_hi(g);
-  const uint64_t g2 = f2_pack(g0, g1);
-  const uint64_t x2 = f2_pack(fminf(fmaxf(g0, -88.0f), 88.0f), fminf(fmaxf(g1, -88.0f), 88.0f));
-  constexpr float kL = 1.44269504088896341f, kLo = static_cast<float>(1.44269504088896341 - static_cast<double>(kL));
-  const uint64_t l2 = f2_pack(-kL, -kL);
-  const uint64_t h2 = f2_mul(x2, l2);
-  float h0, h1;
-  f2_unpack(h2, h0, h1);
-  const uint64_t err2 = f2_fma(x2, l2, f2_pack(-h0, -h1));
-  const uint64_t lo2 = f2_fma(x2, f2_pack(-kLo, -kLo), err2);
-  float e0, e1;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(h0));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(h1));
-  const uint64_t e2 = f2_pack(e0, e1);
-  constexpr float kLn2 = 0.693147180559945309f;
-  float d0, d1;  // 1 + exp(-g)
-  f2_unpack(f2_fma(f2_mul(e2, lo2), f2_pack(kLn2, kLn2), e2), d0, d1);
-  d0 = __fadd_rn(1.0f, d0);
-  d1 = __fadd_rn(1.0f, d1);
-  float r0, r1;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d0));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1));
-  float a0, a1;
+  const uint64_t g2 = f2_pack(bf16_lo(g), bf16_hi(g));
+  constexpr float kNegLog2e = -1.44269504088896341f;
+  float x0, x1, r0, r1, a0, a1;
+  f2_unpack(f2_mul(g2, f2_pack(kNegLog2e, kNegLog2e)), x0, x1);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x0));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x1));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(__fadd_rn(1.0f, x0)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(__fadd_rn(1.0f, x1)));
   f2_unpack(f2_mul(f2_mul(g2, f2_pack(r0, r1)), f2_pack(bf16_lo(u), bf16_hi(u))), a0, a1);
   return pack_bf16x2_rn(a0, a1);
 }
 
-// 16 consecutive values of the source row from channel c on (SwiGLU: gate and up).
+// 32 consecutive values of the source row from channel c on, as 16 bf16 pairs.
 template <int SRC>
-struct Raw16 {
-  uint4 g0, g1, u0, u1;
-  __device__ __forceinline__ void load(const __nv_bfloat16* row, int K, int c, bool ok) {
-    g0 = g1 = u0 = u1 = make_uint4(0, 0, 0, 0);
-    if (!ok) return;
-    g0 = ld_nc_v4_l1(row + c);
-    g1 = ld_nc_v4_l1(row + c + 8);
+__device__ __forceinline__ void load_block(const __nv_bfloat16* row, int K, int c, uint32_t (&w)[16]) {
+  uint4 g[4], u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[i] = ld_nc_v4_l1(row + c + 8 * i);
+  if constexpr (SRC == kQexSwiglu) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = ld_nc_v4_l1(row + K + c + 8 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t gs[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
     if constexpr (SRC == kQexSwiglu) {
-      u0 = ld_nc_v4_l1(row + K + c);
-      u1 = ld_nc_v4_l1(row + K + c + 8);
+      const uint32_t us[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[4 * i + j] = silu_mul_pair(gs[j], us[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[4 * i + j] = gs[j];
     }
   }
-  __device__ __forceinline__ void pairs(uint32_t (&w)[8]) const {  // as 8 bf16 pairs
-    const uint32_t g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
-    const uint32_t u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = SRC == kQexSwiglu ? silu_mul_pair(g[i], u[i]) : g[i];
-  }
-};
+}
 
 constexpr int kQexMaxWarps = 8;
 
@@ -478,17 +463,13 @@ __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts(QuantExpert
   extern __shared__ uint8_t qex_sb[];  // the row's scale bytes, kMxZeroBlock for an all-zero block
   pdl_launch_dependents();             // the GEMM that follows may set itself up meanwhile
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = static_cast<int>(blockDim.x >> 5);
-  const int nblk = a.K >> 5, nseg = (nblk + 15) >> 4, nres = a.r >> 5;
+  const int nblk = a.K >> 5, nres = a.r >> 5;
   const int64_t src = blockIdx.x;
   pdl_wait();
   if (SRC == kQexSwiglu && src >= a.p.offsets[a.experts]) return;
   const __nv_bfloat16* row = a.x + src * a.ldx;
   const int64_t cpitch = a.kpad >> 1;
   const int nrows = SRC == kQexTokens ? a.k : 1;
-  const int half = lane & 1;
-  int seg = warp;
-  Raw16<SRC> next;
-  next.load(row, a.K, 32 * (seg * 16 + (lane >> 1)) + 16 * half, seg * 16 + (lane >> 1) < nblk);
   // lane j: sorted row and scale place of the source row's j-th destination (32 at a time)
   auto places = [&](int j0, int& dst, int& sfr) {
     dst = sfr = -1;
@@ -515,29 +496,38 @@ __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts(QuantExpert
     }
   };
   if (warp < nres) outlier(warp);
-  for (; seg < nseg; seg += nwarps) {
-    const int b = seg * 16 + (lane >> 1);
-    uint32_t w[8];
-    next.pairs(w);
-    const int bn = b + 16 * nwarps;
-    next.load(row, a.K, 32 * bn + 16 * half, bn < nblk);
-    const uint32_t mine = __float_as_uint(absmax16_bf16(w));
-    const uint32_t am = max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
-    const uint32_t sb = mx_scale_byte(am);
-    uint64_t p[8];
+  for (int b0 = 32 * warp; b0 < nblk; b0 += 32 * nwarps) {
+    const int b = b0 + lane;
+    uint32_t w[16];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = f2_pack(bf16_lo(w[e]), bf16_hi(w[e]));
-    uint2 cc = mx_encode16(p, mx_inv_scale(sb));
-    if (am == 0u) cc = make_uint2(0u, 0u);
-    if (nres > 0 && b < nblk && !half) qex_sb[b] = static_cast<uint8_t>(am == 0u ? kMxZeroBlock : sb);
-    // four lane pairs' scale bytes make one 32-bit word, in lanes 0, 8, 16, 24
+    for (int i = 0; i < 16; ++i) w[i] = 0u;
+    if (b < nblk) load_block<SRC>(row, a.K, 32 * b, w);
+    uint32_t mw = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mw = __vmaxu2(mw, w[i] & 0x7FFF7FFFu);
+    const uint32_t am = max(mw & 0xFFFFu, mw >> 16) << 16;
+    const uint32_t sb = mx_scale_byte(am);
+    const float inv = mx_inv_scale(sb);
+    uint4 cc = make_uint4(0u, 0u, 0u, 0u);
+    if (am != 0u) {
+      uint64_t p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = f2_pack(bf16_lo(w[e]), bf16_hi(w[e]));
+      const uint2 lo = mx_encode16(p, inv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = f2_pack(bf16_lo(w[8 + e]), bf16_hi(w[8 + e]));
+      const uint2 hi = mx_encode16(p, inv);
+      cc = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+    if (nres > 0 && b < nblk) qex_sb[b] = static_cast<uint8_t>(am == 0u ? kMxZeroBlock : sb);
+    // four lanes' scale bytes make one 32-bit word, in every fourth lane
     uint32_t sw = sb;
-    sw |= __shfl_down_sync(0xFFFFFFFFu, sw, 2) << 8;
-    sw |= __shfl_down_sync(0xFFFFFFFFu, sw, 4) << 16;
+    sw |= __shfl_down_sync(0xFFFFFFFFu, sw, 1) << 8;
+    sw |= __shfl_down_sync(0xFFFFFFFFu, sw, 2) << 16;
     const bool whole = (b & ~3) + 3 < nblk;  // the word's four blocks exist
-    // the last segment also zeroes the block that pads an odd number of blocks to K_pad
+    // the last lane of the row also zeroes the block that pads an odd number of blocks to K_pad
     const int kbz = nblk + nres;
-    const bool pad = seg == nseg - 1 && 32 * kbz < a.kpad;
+    const bool pad = b == nblk - 1 && 32 * kbz < a.kpad;
     for (int j0 = 0; j0 < nrows; j0 += 32) {
       int dsts = dst0, sfrs = sfr0;
       if (j0) places(j0, dsts, sfrs);
@@ -547,13 +537,13 @@ __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts(QuantExpert
         const int64_t m = __shfl_sync(0xFFFFFFFFu, sfrs, j);
         if (dst < 0) continue;
         uint8_t* crow = a.codes + dst * cpitch;
-        if (b < nblk) *reinterpret_cast<uint2*>(crow + 16 * b + 8 * half) = cc;
+        if (b < nblk) *reinterpret_cast<uint4*>(crow + 16 * b) = cc;
         if (whole) {
-          if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(sf_at(m, b)) = sw;
-        } else if (b < nblk && !half) {
+          if ((lane & 3) == 0) *reinterpret_cast<uint32_t*>(sf_at(m, b)) = sw;
+        } else if (b < nblk) {
           *sf_at(m, b) = static_cast<uint8_t>(sb);
         }
-        if (pad && lane == 0) {
+        if (pad) {
           *reinterpret_cast<uint4*>(crow + 16 * kbz) = make_uint4(0, 0, 0, 0);
           *sf_at(m, kbz) = 0;
         }

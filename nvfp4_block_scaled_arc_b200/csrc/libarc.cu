@@ -457,8 +457,8 @@ arc_status quantize_experts(const void* x, int64_t ldx, int64_t K, const int32_t
   a.experts = experts;
   a.codes = codes;
   a.sf = sf;
-  // as many warps as the row has segments of 512 values, or as divide them into the fewest rounds
-  const int nseg = static_cast<int>((K / 32 + 15) / 16);
+  // as many warps as the row has segments of 1024 values, or as divide them into the fewest rounds
+  const int nseg = static_cast<int>((K / 32 + 31) / 32);
   const int rounds = (nseg + arc::kQexMaxWarps - 1) / arc::kQexMaxWarps;
   const int warps = (nseg + rounds - 1) / rounds;
   return launch_pdl(arc::k_quant_experts<SRC>, a.n, 32 * warps, r > 0 ? static_cast<size_t>(K / 32) : 0, 1, S(stream),
