@@ -260,23 +260,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
   pdl_wait();  // the plan and the operands come from earlier kernels
+  for (int e = threadIdx.x; e <= g.experts; e += kGemmThreads) offsets[e] = g.p.offsets[e];
+  __syncthreads();
   if (warp == 2) {
     // first row tile of every expert: exclusive sum of ceil(rows / TN)
     int run = 0;
     for (int e0 = 0; e0 <= g.experts; e0 += 32) {
       const int e = e0 + lane;
-      const int at = g.p.offsets[min(e, g.experts)], next = g.p.offsets[min(e + 1, g.experts)];
-      const int n = (next - at + T::TN - 1) / T::TN;
+      const int n = e < g.experts ? (offsets[e + 1] - offsets[e] + T::TN - 1) / T::TN : 0;
       int inc = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
         if (lane >= o) inc += v;
       }
-      if (e <= g.experts) {
-        first[e] = run + inc - n;
-        offsets[e] = at;
-      }
+      if (e <= g.experts) first[e] = run + inc - n;
       run += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
   }
