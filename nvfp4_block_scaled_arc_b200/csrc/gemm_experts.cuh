@@ -38,20 +38,23 @@
 
 namespace arc {
 
-template <int KIND>
+// MAXN: rows of a tile, at most. 256 is the general form; 64 (few rows for each expert, where reading the
+// weights is the work) leaves room for more stages in flight and for more accumulators.
+template <int KIND, int MAXN>
 struct ExpertGemmTraits {
   static constexpr bool MX4 = KIND == kGemmMX4;
   static constexpr int BM = 128, TM = 256;  // features of a CTA and of the pair
-  static constexpr int TN = 256;            // rows of a tile, at most
+  static constexpr int TN = MAXN;
   static constexpr int W_BYTES = BM * 128, X_BYTES = TN / 2 * 128;
   static constexpr int SFW_BYTES = MX4 ? 2 * 512 : 0, SFX_BYTES = MX4 ? TN * 8 : 0;
-  static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + SFW_BYTES + SFX_BYTES;
-  static constexpr int STAGES = 6;
-  static constexpr int ACC_STAGES = MX4 ? 1 : 2;
-  static constexpr int SF_COL0 = 256, SF_SET_COLS = 32;
+  static constexpr int STAGE_BYTES = (W_BYTES + X_BYTES + SFW_BYTES + SFX_BYTES + 1023) / 1024 * 1024;
+  static constexpr int STAGES = TN == 256 ? 6 : MX4 ? 9 : 10;
+  static constexpr int ACC_STAGES = TN == 256 ? (MX4 ? 1 : 2) : 3;
+  static constexpr int SF_COL0 = ACC_STAGES * TN, SF_SET_COLS = 32;
   static constexpr uint32_t IDESC0 = MX4 ? idesc_mxf4(TM, 0) : idesc_bf16(TM, 0);  // N is the tile's
   // scale-factor ids of the second K = 64 step of an atom (bytes 2 and 3 of a cell)
   static constexpr uint32_t ODD_STEP = MX4 ? (2u << 29) | (2u << 4) : 0u;
+  static_assert(SF_COL0 + (MX4 ? STAGES * SF_SET_COLS : 0) <= 512, "tensor memory");
 };
 
 constexpr int kExpertEpiBytes = 16 * 32 * 2;  // 16 rows of Y x 32 features, one per epilogue warp
@@ -61,11 +64,13 @@ constexpr int kRowBoxes = 9;
 __host__ __device__ constexpr int row_box_index(int rows) { return rows <= 8 ? 0 : (rows + 15) / 16; }
 __host__ __device__ constexpr int row_box_height(int index) { return index == 0 ? 8 : 16 * index; }
 
-// Shared memory behind the stages: staging, barriers (256 B), first tile and first row of every expert.
-template <int KIND>
+constexpr int kExpertBarBytes = 384;
+
+// Shared memory behind the stages: staging, barriers, first tile and first row of every expert.
+template <int KIND, int MAXN>
 constexpr int expert_gemm_smem_bytes(int experts) {
-  return ExpertGemmTraits<KIND>::STAGES * ExpertGemmTraits<KIND>::STAGE_BYTES + 8 * kExpertEpiBytes + 256 +
-         2 * (experts + 1) * 4 + 1024;
+  return ExpertGemmTraits<KIND, MAXN>::STAGES * ExpertGemmTraits<KIND, MAXN>::STAGE_BYTES + 8 * kExpertEpiBytes +
+         kExpertBarBytes + 2 * (experts + 1) * 4 + 1024;
 }
 
 struct ExpertGemmArgs {
@@ -142,10 +147,9 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
       : "memory");
 }
 
-template <int KIND>
+template <class T>
 __device__ __forceinline__ void expert_mma(uint32_t d_tmem, uint64_t dw, uint64_t dx, uint32_t idesc, uint32_t sf, int k,
                                            uint32_t accum) {
-  using T = ExpertGemmTraits<KIND>;
   if constexpr (T::MX4) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -218,11 +222,11 @@ __device__ __forceinline__ ExpertTile expert_tile(int t, const int* first, const
   return r;
 }
 
-template <int KIND>
+template <int KIND, int MAXN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_gemm_experts(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ ExpertRowMaps tmX,
                    const __grid_constant__ CUtensorMap tmY, const ExpertGemmArgs g) {
-  using T = ExpertGemmTraits<KIND>;
+  using T = ExpertGemmTraits<KIND, MAXN>;
   constexpr bool MX4 = T::MX4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -231,13 +235,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint64_t* empty = full + T::STAGES;
   uint64_t* ready = empty + T::STAGES;
   uint64_t* acc_full = ready + T::STAGES;
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* acc_empty = acc_full + T::ACC_STAGES;
+  uint64_t* drain = acc_empty + T::ACC_STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* first = reinterpret_cast<int*>(staging + 8 * kExpertEpiBytes + 256);  // [E + 1]
+  int* first = reinterpret_cast<int*>(staging + 8 * kExpertEpiBytes + kExpertBarBytes);  // [E + 1]
   int* offsets = first + g.experts + 1;                                      // [E + 1]
-  static_assert((3 * T::STAGES + 5) * 8 + 8 <= 256, "barriers");
+  static_assert((3 * T::STAGES + 2 * T::ACC_STAGES + 1) * 8 + 8 <= kExpertBarBytes, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_cta_rank();
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(&empty[s], 1);
       mbar_init(&ready[s], MX4 ? 8 : 2);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < T::ACC_STAGES; ++a) {
       mbar_init(&acc_full[a], 1);
       mbar_init(&acc_empty[a], 16);
     }
@@ -367,10 +371,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (nk == 4) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                expert_mma<KIND>(d_tmem, dw + 2 * k, dx + 2 * k, idesc, sf, k, k > 0 ? 1u : acc0);
+                expert_mma<T>(d_tmem, dw + 2 * k, dx + 2 * k, idesc, sf, k, k > 0 ? 1u : acc0);
             } else {
               for (int k = 0; k < nk; ++k)
-                expert_mma<KIND>(d_tmem, dw + 2 * k, dx + 2 * k, idesc, sf, k, k > 0 ? 1u : acc0);
+                expert_mma<T>(d_tmem, dw + 2 * k, dx + 2 * k, idesc, sf, k, k > 0 ? 1u : acc0);
             }
             tc_commit_pair(&empty[stage]);
             if (ks == g.kstages - 1) tc_commit_pair(&acc_full[acc]);
@@ -461,7 +465,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           // value that reaches a stored result
           uint32_t v[16];
 #pragma unroll
-          for (int r = 0; r < 8; ++r) lds_u32x2(sSFX + (32 * r + lane) * 8, v[r], v[8 + r]);
+          for (int r = 0; r < 8; ++r)
+            if (32 * r < T::TN) lds_u32x2(sSFX + (32 * r + lane) * 8, v[r], v[8 + r]);
+            else v[r] = v[8 + r] = 0u;
           const uint32_t w0 = lds_u32(sSFW + lane * 16 + 4 * q), w1 = lds_u32(sSFW + 512 + lane * 16 + 4 * q);
           tmem_st_32x32b_x16(set, v);
           tmem_st_32x32b_x1(set + 16 + q, w0);
@@ -493,9 +499,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!__all_sync(0xFFFFFFFFu, got)) break;
       tc_fence_after();
       const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * T::TN + half * 16;
-      uint32_t pk[64];
+      constexpr int NC = T::TN / 32;  // 16-row chunks of a warp
+      uint32_t pk[8 * NC];
 #pragma unroll
-      for (int c = 0; c < 8; c += 2) {
+      for (int c = 0; c < NC; c += 2) {
         if (32 * c + 16 * half < at.n) {
           uint32_t r0[16], r1[16];
           tmem_ld_32x32b_x16(tbase + 32 * c, r0);
@@ -512,7 +519,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&acc_empty[acc], 0);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < NC; ++c) {
         const int r0 = 32 * c + 16 * half;  // first row of the chunk within the tile
         const int nrows = at.left - r0;
         if (r0 < at.n && nrows > 0 && f0 < g.N) {

@@ -70,10 +70,14 @@ arc_status device_check(int* sms) {
                              arc::gemm_smem_bytes<arc::kGemmMX4>()) != cudaSuccess ||
         cudaFuncSetAttribute(arc::k_gemm<arc::kGemmMX4, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              arc::gemm_smem_bytes<arc::kGemmMX4>()) != cudaSuccess ||
-        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             arc::expert_gemm_smem_bytes<arc::kGemmMX4>(arc::kMaxExperts)) != cudaSuccess ||
-        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmBF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             arc::expert_gemm_smem_bytes<arc::kGemmBF16>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmMX4, 64>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmMX4, 256>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmBF16, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmBF16, 64>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmBF16, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmBF16, 256>(arc::kMaxExperts)) != cudaSuccess ||
         cudaFuncSetAttribute(arc::k_expert_plan<int32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(arc::plan_smem_bytes(arc::kMaxExperts))) != cudaSuccess ||
         cudaFuncSetAttribute(arc::k_expert_plan<int64_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -465,11 +469,11 @@ arc_status quantize_experts(const void* x, int64_t ldx, int64_t K, const int32_t
                     a);
 }
 
-template <int KIND>
-arc_status expert_gemm(const void* a, int64_t a_pitch, const uint8_t* a_sf, const void* b, int64_t b_pitch,
+template <int KIND, int MAXN>
+arc_status expert_gemm_launch(const void* a, int64_t a_pitch, const uint8_t* a_sf, const void* b, int64_t b_pitch,
                        const uint8_t* b_sf, const int32_t* plan, int64_t tokens, int32_t k, int32_t experts, int64_t N,
                        int64_t K, void* y, int64_t ldy, arc_stream_t stream) {
-  using T = arc::ExpertGemmTraits<KIND>;
+  using T = arc::ExpertGemmTraits<KIND, MAXN>;
   constexpr bool MX4 = T::MX4;
   int sms = 0;
   arc_status st = device_check(&sms);
@@ -511,8 +515,19 @@ arc_status expert_gemm(const void* a, int64_t a_pitch, const uint8_t* a_sf, cons
   // the most tiles that the routing can make; the kernel reads the real number from the plan
   const int64_t max_tiles = (slots + (T::TN - 1) * std::min<int64_t>(experts, slots)) / T::TN * g.tiles_w;
   g.inject = take_inject(1);
-  return launch_pdl(arc::k_gemm_experts<KIND>, 2 * std::min<int64_t>(max_tiles, sms / 2), arc::kGemmThreads,
-                    arc::expert_gemm_smem_bytes<KIND>(experts), 2, S(stream), tw, tx, ty, g);
+  return launch_pdl(arc::k_gemm_experts<KIND, MAXN>, 2 * std::min<int64_t>(max_tiles, sms / 2), arc::kGemmThreads,
+                    arc::expert_gemm_smem_bytes<KIND, MAXN>(experts), 2, S(stream), tw, tx, ty, g);
+}
+
+template <int KIND>
+arc_status expert_gemm(const void* a, int64_t a_pitch, const uint8_t* a_sf, const void* b, int64_t b_pitch,
+                       const uint8_t* b_sf, const int32_t* plan, int64_t tokens, int32_t k, int32_t experts, int64_t N,
+                       int64_t K, void* y, int64_t ldy, arc_stream_t stream) {
+  const bool few = tokens * k <= 32ll * experts;
+  return few ? expert_gemm_launch<KIND, 64>(a, a_pitch, a_sf, b, b_pitch, b_sf, plan, tokens, k, experts, N, K, y, ldy,
+                                            stream)
+             : expert_gemm_launch<KIND, 256>(a, a_pitch, a_sf, b, b_pitch, b_sf, plan, tokens, k, experts, N, K, y,
+                                             ldy, stream);
 }
 
 }  // namespace
