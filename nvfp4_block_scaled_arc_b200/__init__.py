@@ -553,27 +553,38 @@ class ExpertPlan:
     sections that include/arc.h describes, seen through offsets, blocks, row_of_slot, slot_of_row and
     sf_row. Made by expert_plan, or put around a buffer of that layout."""
 
-    __slots__ = ("buf", "tokens", "k", "experts")
+    __slots__ = ("buf", "tokens", "k", "experts", "slots")
 
     def __init__(self, buf: torch.Tensor, tokens: int, k: int, experts: int):
-        if buf.numel() < 2 * _pad64(experts + 1) + 3 * _pad64(tokens * k) or not buf.is_contiguous():
+        slots = tokens * k
+        if (buf.dtype is not torch.int32 or not buf.is_contiguous() or
+                buf.numel() < 2 * _pad64(experts + 1) + 3 * _pad64(slots)):
             raise ValueError("ExpertPlan: the buffer does not hold a plan of these sizes")
-        self.buf, self.tokens, self.k, self.experts = buf, tokens, k, experts
+        self.buf, self.tokens, self.k, self.experts, self.slots = buf, tokens, k, experts, slots
 
     @property
-    def slots(self) -> int:
-        return self.tokens * self.k
+    def offsets(self) -> torch.Tensor:
+        return self.buf[:self.experts + 1]
 
-    def _section(self, i: int, n: int) -> torch.Tensor:
-        head = _pad64(self.experts + 1)
-        at = i * head if i < 2 else 2 * head + (i - 2) * _pad64(self.slots)
-        return self.buf[at:at + n]
+    @property
+    def blocks(self) -> torch.Tensor:
+        at = _pad64(self.experts + 1)
+        return self.buf[at:at + self.experts + 1]
 
-    offsets = property(lambda self: self._section(0, self.experts + 1))
-    blocks = property(lambda self: self._section(1, self.experts + 1))
-    row_of_slot = property(lambda self: self._section(2, self.slots))
-    slot_of_row = property(lambda self: self._section(3, self.slots))
-    sf_row = property(lambda self: self._section(4, self.slots))
+    @property
+    def row_of_slot(self) -> torch.Tensor:
+        at = 2 * _pad64(self.experts + 1)
+        return self.buf[at:at + self.slots]
+
+    @property
+    def slot_of_row(self) -> torch.Tensor:
+        at = 2 * _pad64(self.experts + 1) + _pad64(self.slots)
+        return self.buf[at:at + self.slots]
+
+    @property
+    def sf_row(self) -> torch.Tensor:
+        at = 2 * _pad64(self.experts + 1) + 2 * _pad64(self.slots)
+        return self.buf[at:at + self.slots]
 
 
 @dataclass
@@ -596,7 +607,8 @@ class ExpertWeightMXFP4:
     k_aug: int
 
 
-_current_raw_stream = torch._C._cuda_getCurrentRawStream  # the handle alone; building a Stream object costs 1 us
+# The handles alone: building Stream objects would cost a small call a tenth of its time.
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
@@ -615,9 +627,12 @@ def _refuse(fn: str, name: str, t: torch.Tensor, dtype, dev: int, shape):
 def _rows_of(fn: str, name: str, t: torch.Tensor, dtype, dev: int, shape: tuple) -> int:
     """The leading dimension of a [rows, cols] argument; refuses one of another device, dtype, shape
     or with strided rows. A single row has the row's length, whatever its stride says."""
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or (t.stride(1) != 1 and shape[1] != 1):
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
         _refuse(fn, name, t, dtype, dev, shape)
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    ld, step = t.stride()
+    if step != 1 and shape[1] != 1:
+        _refuse(fn, name, t, dtype, dev, shape)
+    return ld if shape[0] > 1 else shape[1]
 
 
 def _flat(fn: str, name: str, t: torch.Tensor, dtype, dev: int, least: int):
@@ -628,31 +643,22 @@ def _flat(fn: str, name: str, t: torch.Tensor, dtype, dev: int, least: int):
         raise ValueError(f"{fn}: {name} holds {t.numel()} values, {least} are needed")
 
 
-class _on:
-    """The device of a call's tensors as the current one, and the caller's stream (if one is given)
-    as the one that its outputs are allocated for. Yields the stream's handle."""
+def _plan_ptr(fn: str, plan: ExpertPlan, dev: int) -> int:
+    if plan.buf.get_device() != dev:
+        _refuse(fn, "plan", plan.buf, _I32, dev, None)
+    return plan.buf.data_ptr()
 
-    __slots__ = ("ctx", "raw")
 
-    def __init__(self, fn: str, dev: int, stream):
-        if dev < 0:
-            raise ValueError(f"{fn}: tensors must be CUDA tensors")
-        if stream is not None:
-            if stream.device.index != dev:
-                raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on cuda:{dev}")
-            self.ctx, self.raw = torch.cuda.stream(stream), stream.cuda_stream
-        else:
-            self.ctx = None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
-            self.raw = _current_raw_stream(dev)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.raw
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _on(fn: str, dev: int, stream):
+    """Context in which a call on tensors of device `dev` runs when that is not the current device or
+    a stream is given: both become the current ones, so that outputs are allocated for them."""
+    if dev < 0:
+        raise ValueError(f"{fn}: tensors must be CUDA tensors")
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on cuda:{dev}")
+    return torch.cuda.stream(stream)
 
 
 def expert_plan(ids: torch.Tensor, experts: int, out: ExpertPlan | None = None, stream=None) -> ExpertPlan:
@@ -663,31 +669,33 @@ def expert_plan(ids: torch.Tensor, experts: int, out: ExpertPlan | None = None, 
         raise ValueError("expert_plan: ids must be [tokens, k] of int32 or int64")
     shape = ids.shape
     T, k = shape
-    with _on(fn, dev, stream) as raw:
-        ld = _rows_of(fn, "ids", ids, dtype, dev, shape)
-        if out is None:
-            n = 2 * _pad64(experts + 1) + 3 * _pad64(T * k)
-            out = ExpertPlan(torch.empty(n, dtype=_I32, device=ids.device), T, k, experts)
-        elif (out.tokens, out.k, out.experts) != (T, k, experts):
-            raise ValueError("expert_plan: out was made for other sizes")
-        buf = out.buf
-        _flat(fn, "out", buf, _I32, dev, 0)
-        _check("arc_expert_plan", lib().arc_expert_plan(
-            ids.data_ptr(), 4 if dtype is torch.int32 else 8, ld, T, k, experts, buf.data_ptr(), buf.numel() * 4, raw))
+    if stream is not None or dev < 0 or dev != _device():
+        with _on(fn, dev, stream):
+            return expert_plan(ids, experts, out)
+    ld = _rows_of(fn, "ids", ids, dtype, dev, shape)
+    if out is None:
+        n = 2 * _pad64(experts + 1) + 3 * _pad64(T * k)
+        out = ExpertPlan(torch.empty(n, dtype=_I32, device=ids.device), T, k, experts)
+    elif (out.tokens, out.k, out.experts) != (T, k, experts):
+        raise ValueError("expert_plan: out was made for other sizes")
+    _check("arc_expert_plan", lib().arc_expert_plan(
+        ids.data_ptr(), 4 if dtype is _I32 else 8, ld, T, k, experts, _plan_ptr(fn, out, dev), out.buf.numel() * 4,
+        _raw_stream(dev)))
     return out
 
 
 def dispatch_experts(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """arc_dispatch_experts_bf16: tokens x [T, d] bf16 copied into sorted order [S, d]."""
     fn, dev, d, T, k = "dispatch_experts", x.get_device(), x.shape[-1], plan.tokens, plan.k
-    with _on(fn, dev, stream) as raw:
-        ld = _rows_of(fn, "x", x, _BF16, dev, (T, d))
-        _flat(fn, "plan", plan.buf, _I32, dev, 0)
-        if out is None:
-            out = x.new_empty((T * k, d))
-        _check("arc_dispatch_experts_bf16", lib().arc_dispatch_experts_bf16(
-            x.data_ptr(), ld, d, plan.buf.data_ptr(), T, k, plan.experts, out.data_ptr(),
-            _rows_of(fn, "out", out, _BF16, dev, (T * k, d)), raw))
+    if stream is not None or dev < 0 or dev != _device():
+        with _on(fn, dev, stream):
+            return dispatch_experts(x, plan, out)
+    ld = _rows_of(fn, "x", x, _BF16, dev, (T, d))
+    if out is None:
+        out = x.new_empty((T * k, d))
+    _check("arc_dispatch_experts_bf16", lib().arc_dispatch_experts_bf16(
+        x.data_ptr(), ld, d, _plan_ptr(fn, plan, dev), T, k, plan.experts, out.data_ptr(),
+        _rows_of(fn, "out", out, _BF16, dev, (T * k, d)), _raw_stream(dev)))
     return out
 
 
@@ -695,14 +703,15 @@ def dispatch_experts_grad(d_rows: torch.Tensor, plan: ExpertPlan, out: torch.Ten
                           stream=None) -> torch.Tensor:
     """arc_dispatch_experts_grad_bf16: the tokens' gradient [T, d] from the sorted rows' [S, d]."""
     fn, dev, d, T, k = "dispatch_experts_grad", d_rows.get_device(), d_rows.shape[-1], plan.tokens, plan.k
-    with _on(fn, dev, stream) as raw:
-        ld = _rows_of(fn, "d_rows", d_rows, _BF16, dev, (T * k, d))
-        _flat(fn, "plan", plan.buf, _I32, dev, 0)
-        if out is None:
-            out = d_rows.new_empty((T, d))
-        _check("arc_dispatch_experts_grad_bf16", lib().arc_dispatch_experts_grad_bf16(
-            d_rows.data_ptr(), ld, d, plan.buf.data_ptr(), T, k, plan.experts, out.data_ptr(),
-            _rows_of(fn, "out", out, _BF16, dev, (T, d)), raw))
+    if stream is not None or dev < 0 or dev != _device():
+        with _on(fn, dev, stream):
+            return dispatch_experts_grad(d_rows, plan, out)
+    ld = _rows_of(fn, "d_rows", d_rows, _BF16, dev, (T * k, d))
+    if out is None:
+        out = d_rows.new_empty((T, d))
+    _check("arc_dispatch_experts_grad_bf16", lib().arc_dispatch_experts_grad_bf16(
+        d_rows.data_ptr(), ld, d, _plan_ptr(fn, plan, dev), T, k, plan.experts, out.data_ptr(),
+        _rows_of(fn, "out", out, _BF16, dev, (T, d)), _raw_stream(dev)))
     return out
 
 
@@ -711,16 +720,17 @@ def combine_experts(rows: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
     """arc_combine_experts_bf16: y [T, d] = sum over the token's choices of weights [T, k] (fp32) times
     the sorted rows [S, d] (+ add [T, d])."""
     fn, dev, d, T, k = "combine_experts", rows.get_device(), rows.shape[-1], plan.tokens, plan.k
-    with _on(fn, dev, stream) as raw:
-        ld = _rows_of(fn, "rows", rows, _BF16, dev, (T * k, d))
-        ld_w = _rows_of(fn, "weights", weights, _F32, dev, (T, k))
-        _flat(fn, "plan", plan.buf, _I32, dev, 0)
-        if out is None:
-            out = rows.new_empty((T, d))
-        _check("arc_combine_experts_bf16", lib().arc_combine_experts_bf16(
-            rows.data_ptr(), ld, d, weights.data_ptr(), ld_w, plan.buf.data_ptr(), T, k, plan.experts,
-            None if add is None else add.data_ptr(), 0 if add is None else _rows_of(fn, "add", add, _BF16, dev, (T, d)),
-            out.data_ptr(), _rows_of(fn, "out", out, _BF16, dev, (T, d)), raw))
+    if stream is not None or dev < 0 or dev != _device():
+        with _on(fn, dev, stream):
+            return combine_experts(rows, weights, plan, add, out)
+    ld = _rows_of(fn, "rows", rows, _BF16, dev, (T * k, d))
+    ld_w = _rows_of(fn, "weights", weights, _F32, dev, (T, k))
+    if out is None:
+        out = rows.new_empty((T, d))
+    _check("arc_combine_experts_bf16", lib().arc_combine_experts_bf16(
+        rows.data_ptr(), ld, d, weights.data_ptr(), ld_w, _plan_ptr(fn, plan, dev), T, k, plan.experts,
+        None if add is None else add.data_ptr(), 0 if add is None else _rows_of(fn, "add", add, _BF16, dev, (T, d)),
+        out.data_ptr(), _rows_of(fn, "out", out, _BF16, dev, (T, d)), _raw_stream(dev)))
     return out
 
 
@@ -730,19 +740,20 @@ def combine_experts_grad(d_y: torch.Tensor, rows: torch.Tensor, weights: torch.T
     """arc_combine_experts_grad_bf16: (d_rows [S, d] bf16, d_weights [T, k] fp32) from d_y [T, d];
     d_rows may be rows."""
     fn, dev, d, T, k = "combine_experts_grad", rows.get_device(), rows.shape[-1], plan.tokens, plan.k
-    with _on(fn, dev, stream) as raw:
-        ld_dy = _rows_of(fn, "d_y", d_y, _BF16, dev, (T, d))
-        ld = _rows_of(fn, "rows", rows, _BF16, dev, (T * k, d))
-        ld_w = _rows_of(fn, "weights", weights, _F32, dev, (T, k))
-        _flat(fn, "plan", plan.buf, _I32, dev, 0)
-        if d_rows is None:
-            d_rows = rows.new_empty((T * k, d))
-        if d_weights is None:
-            d_weights = weights.new_empty((T, k))
-        _check("arc_combine_experts_grad_bf16", lib().arc_combine_experts_grad_bf16(
-            d_y.data_ptr(), ld_dy, rows.data_ptr(), ld, d, weights.data_ptr(), ld_w, plan.buf.data_ptr(), T, k,
-            plan.experts, d_rows.data_ptr(), _rows_of(fn, "d_rows", d_rows, _BF16, dev, (T * k, d)),
-            d_weights.data_ptr(), _rows_of(fn, "d_weights", d_weights, _F32, dev, (T, k)), raw))
+    if stream is not None or dev < 0 or dev != _device():
+        with _on(fn, dev, stream):
+            return combine_experts_grad(d_y, rows, weights, plan, d_rows, d_weights)
+    ld_dy = _rows_of(fn, "d_y", d_y, _BF16, dev, (T, d))
+    ld = _rows_of(fn, "rows", rows, _BF16, dev, (T * k, d))
+    ld_w = _rows_of(fn, "weights", weights, _F32, dev, (T, k))
+    if d_rows is None:
+        d_rows = rows.new_empty((T * k, d))
+    if d_weights is None:
+        d_weights = weights.new_empty((T, k))
+    _check("arc_combine_experts_grad_bf16", lib().arc_combine_experts_grad_bf16(
+        d_y.data_ptr(), ld_dy, rows.data_ptr(), ld, d, weights.data_ptr(), ld_w, _plan_ptr(fn, plan, dev), T, k,
+        plan.experts, d_rows.data_ptr(), _rows_of(fn, "d_rows", d_rows, _BF16, dev, (T * k, d)),
+        d_weights.data_ptr(), _rows_of(fn, "d_weights", d_weights, _F32, dev, (T, k)), _raw_stream(dev)))
     return d_rows, d_weights
 
 
@@ -756,23 +767,24 @@ def _expert_quantize(fn: str, x: torch.Tensor, plan: ExpertPlan, K: int, idx, ou
     dev, S = x.get_device(), plan.tokens * plan.k
     r = 0 if idx is None else idx.numel()
     kp = _pad64(K + r)
-    with _on(fn, dev, stream) as raw:
-        ld = _rows_of(fn, "x" if rows == plan.tokens else "gu", x, _BF16, dev, (rows, x.shape[-1]))
-        _flat(fn, "plan", plan.buf, _I32, dev, 0)
-        if idx is not None:
-            _flat(fn, "idx", idx, _I32, dev, r)
-        nsf = _expert_sf_bytes(plan, K + r)
-        if out is None:
-            out = ExpertMXFP4(torch.empty((S, kp // 2), dtype=_U8, device=x.device),
-                              torch.empty(nsf, dtype=_U8, device=x.device), S, K + r)
-        else:
-            if out.rows != S or out.k_aug != K + r:
-                raise ValueError(f"{fn}: out was made for other sizes")
-            _flat(fn, "out.codes", out.codes, _U8, dev, S * kp // 2)
-            _flat(fn, "out.sf", out.sf, _U8, dev, nsf)
-        _check("arc_" + fn, getattr(lib(), "arc_" + fn)(
-            x.data_ptr(), ld, K, None if idx is None else idx.data_ptr(), r, plan.buf.data_ptr(), plan.tokens, plan.k,
-            plan.experts, out.codes.data_ptr(), out.sf.data_ptr(), raw))
+    if stream is not None or dev < 0 or dev != _device():
+        with _on(fn, dev, stream):
+            return _expert_quantize(fn, x, plan, K, idx, out, None, rows)
+    ld = _rows_of(fn, "x" if rows == plan.tokens else "gu", x, _BF16, dev, (rows, x.shape[-1]))
+    if idx is not None:
+        _flat(fn, "idx", idx, _I32, dev, r)
+    nsf = _expert_sf_bytes(plan, K + r)
+    if out is None:
+        out = ExpertMXFP4(torch.empty((S, kp // 2), dtype=_U8, device=x.device),
+                          torch.empty(nsf, dtype=_U8, device=x.device), S, K + r)
+    else:
+        if out.rows != S or out.k_aug != K + r:
+            raise ValueError(f"{fn}: out was made for other sizes")
+        _flat(fn, "out.codes", out.codes, _U8, dev, S * kp // 2)
+        _flat(fn, "out.sf", out.sf, _U8, dev, nsf)
+    _check("arc_" + fn, getattr(lib(), "arc_" + fn)(
+        x.data_ptr(), ld, K, None if idx is None else idx.data_ptr(), r, _plan_ptr(fn, plan, dev), plan.tokens, plan.k,
+        plan.experts, out.codes.data_ptr(), out.sf.data_ptr(), _raw_stream(dev)))
     return out
 
 
@@ -809,22 +821,24 @@ def pack_weight_experts_mxfp4(w: torch.Tensor, idx: torch.Tensor | None = None, 
         raise ValueError("pack_weight_experts_mxfp4: w must be [experts, N, K]")
     E, N, K = w.shape
     r = 0 if idx is None else idx.numel()
-    with _on(fn, dev, stream) as raw:
-        ld = _expert_weight_ld(fn, w, dev, E, N, K)
-        if idx is not None:
-            _flat(fn, "idx", idx, _I32, dev, r)
-        kp, nsf = _pad64(K + r), E * mxfp4_sf_bytes(N, K + r)
-        if out is None:
-            out = ExpertWeightMXFP4(torch.empty((E * N, kp // 2), dtype=_U8, device=w.device),
-                                    torch.empty(nsf, dtype=_U8, device=w.device), E, N, K + r)
-        else:
-            if (out.experts, out.n, out.k_aug) != (E, N, K + r):
-                raise ValueError("pack_weight_experts_mxfp4: out was made for other sizes")
-            _flat(fn, "out.codes", out.codes, _U8, dev, E * N * kp // 2)
-            _flat(fn, "out.sf", out.sf, _U8, dev, nsf)
-        _check("arc_pack_weight_experts_mxfp4", lib().arc_pack_weight_experts_mxfp4(
-            w.data_ptr(), E, N, K, ld, None if idx is None else idx.data_ptr(), r, out.codes.data_ptr(),
-            out.sf.data_ptr(), raw))
+    if stream is not None or dev < 0 or dev != _device():
+        with _on(fn, dev, stream):
+            return pack_weight_experts_mxfp4(w, idx, out)
+    ld = _expert_weight_ld(fn, w, dev, E, N, K)
+    if idx is not None:
+        _flat(fn, "idx", idx, _I32, dev, r)
+    kp, nsf = _pad64(K + r), E * mxfp4_sf_bytes(N, K + r)
+    if out is None:
+        out = ExpertWeightMXFP4(torch.empty((E * N, kp // 2), dtype=_U8, device=w.device),
+                                torch.empty(nsf, dtype=_U8, device=w.device), E, N, K + r)
+    else:
+        if (out.experts, out.n, out.k_aug) != (E, N, K + r):
+            raise ValueError("pack_weight_experts_mxfp4: out was made for other sizes")
+        _flat(fn, "out.codes", out.codes, _U8, dev, E * N * kp // 2)
+        _flat(fn, "out.sf", out.sf, _U8, dev, nsf)
+    _check("arc_pack_weight_experts_mxfp4", lib().arc_pack_weight_experts_mxfp4(
+        w.data_ptr(), E, N, K, ld, None if idx is None else idx.data_ptr(), r, out.codes.data_ptr(),
+        out.sf.data_ptr(), _raw_stream(dev)))
     return out
 
 
@@ -835,17 +849,18 @@ def gemm_experts_mxfp4(a: ExpertMXFP4, w: ExpertWeightMXFP4, plan: ExpertPlan, o
     if ka != w.k_aug or w.experts != plan.experts or a.rows != S:
         raise ValueError("gemm_experts_mxfp4: operands of other sizes than the plan's, or of two depths")
     kp = _pad64(ka)
-    with _on(fn, dev, stream) as raw:
-        _flat(fn, "a.codes", a.codes, _U8, dev, S * kp // 2)
-        _flat(fn, "a.sf", a.sf, _U8, dev, _expert_sf_bytes(plan, ka))
-        _flat(fn, "w.codes", w.codes, _U8, dev, w.experts * n * kp // 2)
-        _flat(fn, "w.sf", w.sf, _U8, dev, w.experts * ((n + 127) // 128) * ((kp + 127) // 128) * 512)
-        _flat(fn, "plan", plan.buf, _I32, dev, 0)
-        if out is None:
-            out = torch.empty((S, n), dtype=_BF16, device=a.codes.device)
-        _check("arc_gemm_experts_mxfp4", lib().arc_gemm_experts_mxfp4(
-            a.codes.data_ptr(), a.sf.data_ptr(), w.codes.data_ptr(), w.sf.data_ptr(), plan.buf.data_ptr(), plan.tokens,
-            plan.k, plan.experts, n, ka, out.data_ptr(), _rows_of(fn, "out", out, _BF16, dev, (S, n)), raw))
+    if stream is not None or dev < 0 or dev != _device():
+        with _on(fn, dev, stream):
+            return gemm_experts_mxfp4(a, w, plan, out)
+    _flat(fn, "a.codes", a.codes, _U8, dev, S * kp // 2)
+    _flat(fn, "a.sf", a.sf, _U8, dev, _expert_sf_bytes(plan, ka))
+    _flat(fn, "w.codes", w.codes, _U8, dev, w.experts * n * kp // 2)
+    _flat(fn, "w.sf", w.sf, _U8, dev, w.experts * ((n + 127) // 128) * ((kp + 127) // 128) * 512)
+    if out is None:
+        out = torch.empty((S, n), dtype=_BF16, device=a.codes.device)
+    _check("arc_gemm_experts_mxfp4", lib().arc_gemm_experts_mxfp4(
+        a.codes.data_ptr(), a.sf.data_ptr(), w.codes.data_ptr(), w.sf.data_ptr(), _plan_ptr(fn, plan, dev), plan.tokens,
+        plan.k, plan.experts, n, ka, out.data_ptr(), _rows_of(fn, "out", out, _BF16, dev, (S, n)), _raw_stream(dev)))
     return out
 
 
@@ -856,15 +871,16 @@ def gemm_experts_bf16(rows: torch.Tensor, w: torch.Tensor, plan: ExpertPlan, out
     if w.dim() != 3:
         raise ValueError("gemm_experts_bf16: w must be [experts, N, K]")
     N = w.shape[1]
-    with _on(fn, dev, stream) as raw:
-        ld = _rows_of(fn, "rows", rows, _BF16, dev, (S, K))
-        ld_w = _expert_weight_ld(fn, w, dev, plan.experts, N, K)
-        _flat(fn, "plan", plan.buf, _I32, dev, 0)
-        if out is None:
-            out = rows.new_empty((S, N))
-        _check("arc_gemm_experts_bf16", lib().arc_gemm_experts_bf16(
-            rows.data_ptr(), ld, w.data_ptr(), ld_w, plan.buf.data_ptr(), plan.tokens, plan.k, plan.experts, N, K,
-            out.data_ptr(), _rows_of(fn, "out", out, _BF16, dev, (S, N)), raw))
+    if stream is not None or dev < 0 or dev != _device():
+        with _on(fn, dev, stream):
+            return gemm_experts_bf16(rows, w, plan, out)
+    ld = _rows_of(fn, "rows", rows, _BF16, dev, (S, K))
+    ld_w = _expert_weight_ld(fn, w, dev, plan.experts, N, K)
+    if out is None:
+        out = rows.new_empty((S, N))
+    _check("arc_gemm_experts_bf16", lib().arc_gemm_experts_bf16(
+        rows.data_ptr(), ld, w.data_ptr(), ld_w, _plan_ptr(fn, plan, dev), plan.tokens, plan.k, plan.experts, N, K,
+        out.data_ptr(), _rows_of(fn, "out", out, _BF16, dev, (S, N)), _raw_stream(dev)))
     return out
 
 

@@ -392,9 +392,9 @@ __global__ void __launch_bounds__(kMoveThreads)
 // ---------------------------------------------------------------------------------------------
 // MXFP4 quantization into sorted order (format and arithmetic of k_quant_mx_rows). SRC tokens: the
 // row of a token is coded once and written to the token's k sorted rows. SRC SwiGLU: row i of
-// gate|up gives act = bf16(silu(gate) * up), coded into sorted row
-// i; act never goes to memory. A CTA takes one source row, a lane one block of 32 values (one
-// 16-byte store of codes for each destination). The row's scale bytes stay in shared memory for the appended blocks of 32 outlier
+// gate|up gives act = bf16(silu(gate) * up), coded into sorted row i; act never goes to memory. A
+// CTA takes one source row, a lane one block of 32 values (one 16-byte store of codes for each
+// destination). The row's scale bytes stay in shared memory for the appended blocks of 32 outlier
 // channels, a lane each, whose values are read again (two bytes, or a gate and an up).
 // ---------------------------------------------------------------------------------------------
 

@@ -148,8 +148,8 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
 }
 
 template <class T>
-__device__ __forceinline__ void expert_mma(uint32_t d_tmem, uint64_t dw, uint64_t dx, uint32_t idesc, uint32_t sf, int k,
-                                           uint32_t accum) {
+__device__ __forceinline__ void expert_mma(uint32_t d_tmem, uint64_t dw, uint64_t dx, uint32_t idesc, uint32_t sf,
+                                           int k, uint32_t accum) {
   if constexpr (T::MX4) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const CUtensorMap* map_x = &tmX.box[bi];
       const bool has_sfw = MX4 && 2 * at.tw + static_cast<int>(rank) < g.nblk128;
       const uint8_t* sfx = MX4 ? g.sfx + (128ll * g.p.blocks[at.e] + at.row) * 8 : nullptr;
-      const uint32_t bytes0 = static_cast<uint32_t>(g.box_w + box_x) * 128u + (MX4 ? static_cast<uint32_t>(at.n) * 8u : 0u);
+      const uint32_t bytes0 =
+          static_cast<uint32_t>(g.box_w + box_x) * 128u + (MX4 ? static_cast<uint32_t>(at.n) * 8u : 0u);
       for (int ks = 0; ks < g.kstages; ++ks) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], phase ^ 1u, g.wait_ns, abort_flag))) {
           ok = false;
