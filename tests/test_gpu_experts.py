@@ -36,7 +36,7 @@ def _status_ok():
 @pytest.mark.parametrize("tokens,k,experts,how", [
     (1, 1, 1, "skewed"), (1, 8, 128, "skewed"), (3, 2, 5, "drop"), (130, 3, 7, "drop"), (257, 4, 256, "skewed"),
     (1000, 8, 512, "skewed"), (513, 8, 16, "one"), (4099, 6, 61, "drop"), (16384, 8, 64, "skewed"),
-    (2, 1024, 33, "repeat"), (5000, 1, 3, "repeat")])
+    (2, 1024, 33, "repeat"), (5000, 1, 3, "repeat"), (4096, 1, 2, "repeat"), (40001, 8, 512, "drop")])
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 def test_plan_is_the_stable_sort(tokens, k, experts, how, dtype):
     ids = make_ids(tokens + experts, tokens, k, experts, how)
