@@ -377,8 +377,9 @@ arc_status arc_quantize_act_experts_mxfp4(const void* x_bf16, int64_t ldx, int64
  * The input of the experts' down projection: sorted rows gu [S, 2F] (gate columns first) give
  * act [S, F] = bf16( silu(gate) * up ), the product formed to about 2^-21 relative (2^-18 for
  * gates near -60) before its one rounding, so it can differ from arc_silu_mul_bf16's by a bf16 step
- * where it lies that near to a rounding border; 0 for gate < -87.3. It is quantized as arc_quantize_act_mxfp4 with r residual channels of d_idx
- * (channels of act). One kernel; act is not written. Requires F % 32 == 0 and r as above.
+ * where it lies that near to a rounding border; 0 for gate < -87.3. It is quantized as
+ * arc_quantize_act_mxfp4 would, with r residual channels of d_idx (channels of act). One kernel; act
+ * is not written. Requires F % 32 == 0 and r as above.
  */
 arc_status arc_quantize_swiglu_experts_mxfp4(const void* gu_bf16, int64_t ld_gu, int64_t F, const int32_t* d_idx,
                                              int32_t r, const int32_t* plan, int64_t tokens, int32_t k,

@@ -692,10 +692,11 @@ def dispatch_experts(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None
             return dispatch_experts(x, plan, out)
     ld = _rows_of(fn, "x", x, _BF16, dev, (T, d))
     if out is None:
-        out = x.new_empty((T * k, d))
+        out, ld_out = x.new_empty((T * k, d)), d
+    else:
+        ld_out = _rows_of(fn, "out", out, _BF16, dev, (T * k, d))
     _check("arc_dispatch_experts_bf16", lib().arc_dispatch_experts_bf16(
-        x.data_ptr(), ld, d, _plan_ptr(fn, plan, dev), T, k, plan.experts, out.data_ptr(),
-        _rows_of(fn, "out", out, _BF16, dev, (T * k, d)), _raw_stream(dev)))
+        x.data_ptr(), ld, d, _plan_ptr(fn, plan, dev), T, k, plan.experts, out.data_ptr(), ld_out, _raw_stream(dev)))
     return out
 
 
@@ -708,10 +709,12 @@ def dispatch_experts_grad(d_rows: torch.Tensor, plan: ExpertPlan, out: torch.Ten
             return dispatch_experts_grad(d_rows, plan, out)
     ld = _rows_of(fn, "d_rows", d_rows, _BF16, dev, (T * k, d))
     if out is None:
-        out = d_rows.new_empty((T, d))
+        out, ld_out = d_rows.new_empty((T, d)), d
+    else:
+        ld_out = _rows_of(fn, "out", out, _BF16, dev, (T, d))
     _check("arc_dispatch_experts_grad_bf16", lib().arc_dispatch_experts_grad_bf16(
-        d_rows.data_ptr(), ld, d, _plan_ptr(fn, plan, dev), T, k, plan.experts, out.data_ptr(),
-        _rows_of(fn, "out", out, _BF16, dev, (T, d)), _raw_stream(dev)))
+        d_rows.data_ptr(), ld, d, _plan_ptr(fn, plan, dev), T, k, plan.experts, out.data_ptr(), ld_out,
+        _raw_stream(dev)))
     return out
 
 
@@ -726,11 +729,13 @@ def combine_experts(rows: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
     ld = _rows_of(fn, "rows", rows, _BF16, dev, (T * k, d))
     ld_w = _rows_of(fn, "weights", weights, _F32, dev, (T, k))
     if out is None:
-        out = rows.new_empty((T, d))
+        out, ld_out = rows.new_empty((T, d)), d
+    else:
+        ld_out = _rows_of(fn, "out", out, _BF16, dev, (T, d))
     _check("arc_combine_experts_bf16", lib().arc_combine_experts_bf16(
         rows.data_ptr(), ld, d, weights.data_ptr(), ld_w, _plan_ptr(fn, plan, dev), T, k, plan.experts,
         None if add is None else add.data_ptr(), 0 if add is None else _rows_of(fn, "add", add, _BF16, dev, (T, d)),
-        out.data_ptr(), _rows_of(fn, "out", out, _BF16, dev, (T, d)), _raw_stream(dev)))
+        out.data_ptr(), ld_out, _raw_stream(dev)))
     return out
 
 
@@ -857,10 +862,12 @@ def gemm_experts_mxfp4(a: ExpertMXFP4, w: ExpertWeightMXFP4, plan: ExpertPlan, o
     _flat(fn, "w.codes", w.codes, _U8, dev, w.experts * n * kp // 2)
     _flat(fn, "w.sf", w.sf, _U8, dev, w.experts * ((n + 127) // 128) * ((kp + 127) // 128) * 512)
     if out is None:
-        out = torch.empty((S, n), dtype=_BF16, device=a.codes.device)
+        out, ld_out = torch.empty((S, n), dtype=_BF16, device=a.codes.device), n
+    else:
+        ld_out = _rows_of(fn, "out", out, _BF16, dev, (S, n))
     _check("arc_gemm_experts_mxfp4", lib().arc_gemm_experts_mxfp4(
         a.codes.data_ptr(), a.sf.data_ptr(), w.codes.data_ptr(), w.sf.data_ptr(), _plan_ptr(fn, plan, dev), plan.tokens,
-        plan.k, plan.experts, n, ka, out.data_ptr(), _rows_of(fn, "out", out, _BF16, dev, (S, n)), _raw_stream(dev)))
+        plan.k, plan.experts, n, ka, out.data_ptr(), ld_out, _raw_stream(dev)))
     return out
 
 
@@ -877,10 +884,12 @@ def gemm_experts_bf16(rows: torch.Tensor, w: torch.Tensor, plan: ExpertPlan, out
     ld = _rows_of(fn, "rows", rows, _BF16, dev, (S, K))
     ld_w = _expert_weight_ld(fn, w, dev, plan.experts, N, K)
     if out is None:
-        out = rows.new_empty((S, N))
+        out, ld_out = rows.new_empty((S, N)), N
+    else:
+        ld_out = _rows_of(fn, "out", out, _BF16, dev, (S, N))
     _check("arc_gemm_experts_bf16", lib().arc_gemm_experts_bf16(
         rows.data_ptr(), ld, w.data_ptr(), ld_w, _plan_ptr(fn, plan, dev), plan.tokens, plan.k, plan.experts, N, K,
-        out.data_ptr(), _rows_of(fn, "out", out, _BF16, dev, (S, N)), _raw_stream(dev)))
+        out.data_ptr(), ld_out, _raw_stream(dev)))
     return out
 
 

@@ -54,7 +54,8 @@ def test_plan_of_strided_ids_and_of_ids_beyond_int32():
     ids = wide[:, :4]
     p = arc.expert_plan(ids, 10)
     ref = ids.cpu().numpy()
-    np.testing.assert_array_equal(p.row_of_slot.cpu().numpy(), plan_of(np.where((ref < 0) | (ref > 9), -1, ref), 10)["row_of_slot"])
+    want = plan_of(np.where((ref < 0) | (ref > 9), -1, ref), 10)
+    np.testing.assert_array_equal(p.row_of_slot.cpu().numpy(), want["row_of_slot"])
 
 
 def test_plan_without_any_row():
@@ -188,7 +189,8 @@ def test_gradients_against_differences():
     # dispatch: <g_rows, dispatch(x)> is linear in x, its gradient the summed rows of g_rows
     x, g_rows = whole(T, d).bfloat16(), whole(T * k, d).bfloat16()
     sent = arc.dispatch_experts(x, plan)[:used].double()
-    assert (sent * g_rows[:used].double()).sum() == (arc.dispatch_experts_grad(g_rows, plan).double() * x.double()).sum()
+    d_x = arc.dispatch_experts_grad(g_rows, plan).double()
+    assert (sent * g_rows[:used].double()).sum() == (d_x * x.double()).sum()
 
 
 # ----------------------------------------------------------------------------------- quantization

@@ -284,7 +284,10 @@ def test_withheld_load_times_out_and_recovers(kind, T, E):
         a, w = arc.quantize_act_experts_mxfp4(x, plan), arc.pack_weight_experts_mxfp4(wgu)
     else:
         a = arc.dispatch_experts(x, plan)
-    run = (lambda: arc.gemm_experts_mxfp4(a, w, plan)) if kind == "mxfp4" else (lambda: arc.gemm_experts_bf16(a, wgu, plan))
+
+    def run():
+        return arc.gemm_experts_mxfp4(a, w, plan) if kind == "mxfp4" else arc.gemm_experts_bf16(a, wgu, plan)
+
     good = run()
     torch.cuda.synchronize()
     assert arc.last_device_status() == 0
