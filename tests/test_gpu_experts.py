@@ -68,7 +68,8 @@ def test_plan_without_any_row():
 # ------------------------------------------------------------------------------------------ rows
 
 MOVES = [(1, 8, 128, 4096, "skewed"), (5, 2, 4, 8, "drop"), (67, 3, 9, 264, "drop"), (300, 8, 32, 1032, "repeat"),
-         (33, 40, 64, 72, "skewed"), (1023, 1, 5, 2048, "one"), (129, 6, 61, 4104, "drop")]
+         (33, 40, 64, 72, "skewed"), (1023, 1, 5, 2048, "one"), (129, 6, 61, 4104, "drop"), (9, 3, 512, 8, "drop"),
+         (5000, 2, 8, 1032, "drop")]
 
 
 def _inputs(tokens, k, experts, d, how, pad=0):
@@ -373,7 +374,8 @@ def _check_product(y, a, w_of, p, N, K, pad_value=None):
 PRODUCTS = [(1, 2, 8, 64, 8, 0, "skewed"), (1, 8, 64, 512, 264, 32, "skewed"), (37, 3, 5, 96, 200, 32, "drop"),
             (64, 4, 32, 1056, 520, 0, "skewed"), (300, 1, 3, 224, 256, 32, "one"), (257, 2, 4, 512, 768, 64, "drop"),
             (600, 2, 2, 4096, 264, 128, "repeat"), (900, 3, 7, 320, 1032, 0, "skewed"),
-            (129, 1, 1, 256, 256, 32, "one"), (1500, 2, 5, 1024, 520, 96, "drop")]
+            (129, 1, 1, 256, 256, 32, "one"), (1500, 2, 5, 1024, 520, 96, "drop"), (40, 6, 512, 128, 72, 0, "drop"),
+            (65, 1, 1, 64, 8, 0, "one"), (257, 1, 1, 32, 128, 0, "one"), (33, 2, 2, 288, 384, 0, "one")]
 
 
 @pytest.mark.parametrize("tokens,k,experts,K,N,r,how", PRODUCTS)
@@ -409,6 +411,79 @@ def test_bf16_product(tokens, k, experts, K, N, r, how):
     _status_ok()
     av = O.bf16_bits_to_f32(xb).astype(np.float64)[p["slot_of_row"][: p["used"]] // k]
     _check_product(y, av, lambda e: O.bf16_bits_to_f32(wb[e * N:(e + 1) * N]).astype(np.float64), p, N, K)
+
+
+def test_bf16_product_of_eight_channels():
+    rows = torch.ones(3, 8, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(2, 8, 8, dtype=torch.bfloat16, device="cuda")
+    w[1] = 2
+    plan = arc.expert_plan(torch.tensor([[1], [0], [1]], device="cuda"), 2)
+    assert arc.gemm_experts_bf16(rows, w, plan).tolist() == [[8.0] * 8, [16.0] * 8, [16.0] * 8]
+
+
+def test_neighbours_in_a_tile_do_not_meet():
+    # rows and experts of NaN and infinity lie in the same tiles as finite ones: they reach their own
+    # results alone
+    T, E, K, N = 300, 3, 192, 200
+    ids = make_ids(21, T, 1, E)
+    p, plan = plan_of(ids, E), _plan(ids, E)
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    w = torch.randn(E, N, K, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    want = arc.gemm_experts_bf16(arc.dispatch_experts(x, plan), w, plan)
+    want4 = arc.gemm_experts_mxfp4(arc.quantize_act_experts_mxfp4(x, plan), arc.pack_weight_experts_mxfp4(w), plan)
+    x[5], x[17, 3], x[200] = float("nan"), float("inf"), 3e38
+    w[1] = float("nan")
+    w[2, 7] = float("inf")
+    rows = arc.dispatch_experts(x, plan)
+    got = arc.gemm_experts_bf16(rows, w, plan)
+    fine = np.ones((T, N), bool)
+    fine[p["row_of_slot"][[5, 17, 200]]] = False
+    fine[p["expert"] == 1] = False
+    fine[p["expert"] == 2, 7] = False
+    fine = torch.from_numpy(fine).cuda()
+    assert torch.equal(got[fine], want[fine])
+    assert torch.isnan(got[plan.row_of_slot[5]]).all()
+    assert torch.isnan(got[torch.from_numpy(p["expert"] == 1).cuda()]).all()
+    # MXFP4: codes of such rows are not specified, other rows keep their results
+    wq = arc.pack_weight_experts_mxfp4(torch.where(torch.isfinite(w), w, torch.full_like(w, 3e38)))
+    got = arc.gemm_experts_mxfp4(arc.quantize_act_experts_mxfp4(x, plan), wq, plan)
+    # (an expert with a changed weight keeps its other features: one scale block is one feature's)
+    assert torch.equal(got[fine], want4[fine])
+
+
+def test_gpu_refusals():
+    plan = arc.expert_plan(torch.zeros(4, 2, dtype=torch.int32, device="cuda"), 3)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    rows = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(3, 64, 64, dtype=torch.bfloat16, device="cuda")
+    wt = torch.zeros(4, 2, device="cuda")
+    a, q = arc.quantize_act_experts_mxfp4(x, plan), arc.pack_weight_experts_mxfp4(w)
+    refused = [
+        lambda: arc.dispatch_experts(x[:3], plan), lambda: arc.dispatch_experts(x.float(), plan),
+        lambda: arc.dispatch_experts(x.t().contiguous().t(), plan), lambda: arc.dispatch_experts(x, plan, out=rows[:4]),
+        lambda: arc.dispatch_experts_grad(rows[:7], plan), lambda: arc.combine_experts(rows, wt.half(), plan),
+        lambda: arc.combine_experts(rows, wt[:, :1], plan), lambda: arc.combine_experts(rows, wt, plan, add=rows),
+        lambda: arc.combine_experts_grad(rows, rows, wt, plan), lambda: arc.combine_experts(rows, wt.cpu(), plan),
+        lambda: arc.quantize_act_experts_mxfp4(rows, plan), lambda: arc.quantize_swiglu_experts_mxfp4(x, plan),
+        lambda: arc.quantize_act_experts_mxfp4(x, plan, torch.arange(32, device="cuda")),
+        lambda: arc.quantize_act_experts_mxfp4(x, plan, out=arc.ExpertMXFP4(a.codes, a.sf[:-1], 8, 64)),
+        lambda: arc.gemm_experts_bf16(rows, w[:2], plan), lambda: arc.gemm_experts_bf16(rows, w[:, :, :32], plan),
+        lambda: arc.gemm_experts_bf16(rows, torch.zeros(6, 64, 64, dtype=torch.bfloat16, device="cuda")[::2], plan),
+        lambda: arc.gemm_experts_mxfp4(a, arc.ExpertWeightMXFP4(q.codes[:-1], q.sf, 3, 64, 64), plan),
+        lambda: arc.gemm_experts_mxfp4(a, arc.ExpertWeightMXFP4(q.codes, q.sf[:-1], 3, 64, 64), plan),
+        lambda: arc.expert_plan(torch.zeros(4, 2, dtype=torch.int32, device="cuda"), 4, out=plan)]
+    for i, call in enumerate(refused):
+        with pytest.raises(ValueError):
+            call()
+            raise AssertionError(i)
+    for call in (lambda: arc.dispatch_experts(x[:, :60], plan),
+                 lambda: arc.expert_plan(plan.offsets[:2].view(2, 1), 513),
+                 lambda: arc.gemm_experts_bf16(rows, w[:, :60].contiguous(), plan),
+                 lambda: arc.quantize_act_experts_mxfp4(x, plan, torch.arange(16, dtype=torch.int32, device="cuda")),
+                 lambda: arc.expert_plan(torch.zeros(0, 2, dtype=torch.int32, device="cuda"), 3)):
+        with pytest.raises(arc.ArcError):
+            call()
+    _status_ok()
 
 
 def test_products_repeat_bit_for_bit():
