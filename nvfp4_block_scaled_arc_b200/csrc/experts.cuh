@@ -37,6 +37,28 @@ __host__ __device__ inline Plan plan_sections(const int32_t* p, int64_t slots, i
   return v;
 }
 
+// Loads of what an earlier kernel may have written. These kernels begin while that kernel still runs
+// and wait for it (griddepcontrol.wait); a non-coherent load, or a plain one through a pointer to
+// const that is __restrict__, counts as constant for the whole kernel and could be moved before
+// that wait, so there is none here.
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_v4_once(const void* p) {  // read once: not kept in L1
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_u16(const void* p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+
 // ---------------------------------------------------------------------------------------------
 // Plan, in one launch without a grid-wide wait. The slots are cut into parts, one for each cluster
 // of CTAs. A cluster counts the ids of all slots per expert (4 bytes a slot from L2, spread over
@@ -82,7 +104,7 @@ __device__ __forceinline__ uint32_t same_expert(int e, int bits) {
 
 template <typename ID>
 __global__ void __launch_bounds__(kPlanThreads, 1)
-    k_expert_plan(const ID* __restrict__ ids, int64_t ld, int slots, int k, int experts, int ctas, int32_t* plan) {
+    k_expert_plan(const ID* ids, int64_t ld, int slots, int k, int experts, int ctas, int32_t* plan) {
   namespace cg = cooperative_groups;
   extern __shared__ int32_t plan_sm[];
   __shared__ int32_t scan_rows[kPlanWarps], scan_blocks[kPlanWarps];
@@ -248,9 +270,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 constexpr int kMoveThreads = 256;
 
 template <int U>
-__global__ void __launch_bounds__(kMoveThreads) k_dispatch(const __nv_bfloat16* __restrict__ x, int64_t ldx, int vecs,
+__global__ void __launch_bounds__(kMoveThreads) k_dispatch(const __nv_bfloat16* x, int64_t ldx, int vecs,
                                                            Plan p, int64_t tokens, int k,
-                                                           __nv_bfloat16* __restrict__ rows, int64_t ldr) {
+                                                           __nv_bfloat16* rows, int64_t ldr) {
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int nseg = (vecs + 32 * U - 1) / (32 * U);
@@ -262,7 +284,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_dispatch(const __nv_bfloat16* 
   uint4 w[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    w[u] = v0 + 32 * u < vecs ? ld_nc_v4(x + t * ldx + 8 * (v0 + 32 * u)) : make_uint4(0, 0, 0, 0);
+    w[u] = v0 + 32 * u < vecs ? ld_v4_once(x + t * ldx + 8 * (v0 + 32 * u)) : make_uint4(0, 0, 0, 0);
   for (int j0 = 0; j0 < k; j0 += 32) {
     const int nj = min(32, k - j0);
     const int mine = lane < nj ? p.row_of_slot[t * k + j0 + lane] : -1;
@@ -292,7 +314,7 @@ __device__ __forceinline__ void fma_bf16x8(float (&acc)[8], float w, uint4 v) {
 // nullptr) the gradient of the dispatch.
 template <int U>
 __global__ void __launch_bounds__(kMoveThreads)
-    k_combine(const __nv_bfloat16* __restrict__ rows, int64_t ldr, int vecs, const float* __restrict__ weights,
+    k_combine(const __nv_bfloat16* rows, int64_t ldr, int vecs, const float* weights,
               int64_t ldw, Plan p, int64_t tokens, int k, const __nv_bfloat16* add, int64_t lda, __nv_bfloat16* y,
               int64_t ldy) {
   pdl_launch_dependents();
@@ -320,7 +342,7 @@ __global__ void __launch_bounds__(kMoveThreads)
       const __nv_bfloat16* src = rows + row * ldr;
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (v0 + 32 * u < vecs) fma_bf16x8(acc[u], w, ld_nc_v4(src + 8 * (v0 + 32 * u)));
+        if (v0 + 32 * u < vecs) fma_bf16x8(acc[u], w, ld_v4_once(src + 8 * (v0 + 32 * u)));
     }
   }
 #pragma unroll
@@ -339,9 +361,9 @@ __global__ void __launch_bounds__(kMoveThreads)
 // by lane, joined by shuffles: a fixed order). d_rows may be rows: each vector is read before the
 // same lane writes it.
 __global__ void __launch_bounds__(kMoveThreads)
-    k_combine_grad(const __nv_bfloat16* __restrict__ dy, int64_t lddy, const __nv_bfloat16* rows, int64_t ldr,
-                   int vecs, const float* __restrict__ weights, int64_t ldw, Plan p, int64_t tokens, int k,
-                   __nv_bfloat16* d_rows, int64_t lddr, float* __restrict__ d_w, int64_t lddw) {
+    k_combine_grad(const __nv_bfloat16* dy, int64_t lddy, const __nv_bfloat16* rows, int64_t ldr,
+                   int vecs, const float* weights, int64_t ldw, Plan p, int64_t tokens, int k,
+                   __nv_bfloat16* d_rows, int64_t lddr, float* d_w, int64_t lddw) {
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t s = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
@@ -366,7 +388,7 @@ __global__ void __launch_bounds__(kMoveThreads)
       const int v = v0 + 32 * u;
       g[u] = r[u] = make_uint4(0, 0, 0, 0);
       if (v < vecs) {
-        g[u] = ld_nc_v4_l1(a + 8 * v);
+        g[u] = ld_v4(a + 8 * v);
         r[u] = *reinterpret_cast<const uint4*>(b + 8 * v);
       }
     }
@@ -437,10 +459,10 @@ template <int SRC>
 __device__ __forceinline__ void load_block(const __nv_bfloat16* row, int K, int c, uint32_t (&w)[16]) {
   uint4 g[4], u[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) g[i] = ld_nc_v4_l1(row + c + 8 * i);
+  for (int i = 0; i < 4; ++i) g[i] = ld_v4(row + c + 8 * i);
   if constexpr (SRC == kQexSwiglu) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = ld_nc_v4_l1(row + K + c + 8 * i);
+    for (int i = 0; i < 4; ++i) u[i] = ld_v4(row + K + c + 8 * i);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -488,8 +510,8 @@ __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts(QuantExpert
   auto outlier = [&](int rb) {
     oc = a.idx[32 * rb + lane];
     if (static_cast<unsigned>(oc) < static_cast<unsigned>(a.K)) {
-      og = ldg_nc_u16(row + oc);
-      if constexpr (SRC == kQexSwiglu) ou = ldg_nc_u16(row + a.K + oc);
+      og = ld_u16(row + oc);
+      if constexpr (SRC == kQexSwiglu) ou = ld_u16(row + a.K + oc);
     } else {
       oc = -1;
       if (src == 0) set_status(kStatusInvalidArg);
