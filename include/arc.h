@@ -314,6 +314,10 @@ arc_status arc_gemm_mxfp4(const uint8_t* a_codes, const uint8_t* a_sf, const uin
  * Packed weights of E experts: codes [E * N, K_pad/2]; scale bytes of expert e at
  * e * arc_mxfp4_sf_bytes(N, K + r).
  *
+ * A plan's entries are checked on the device against the buffers' sizes: one that lies outside sets
+ * the status word (ARC_ERR_INVALID_ARG) and is treated as no row, a product over such a plan writes
+ * nothing.
+ *
  * Limits of every call of this section: 1 <= E <= 512, 1 <= k <= 1024, 1 <= T, S <= 2^28.
  */
 size_t arc_expert_plan_bytes(int64_t tokens, int32_t k, int32_t experts);

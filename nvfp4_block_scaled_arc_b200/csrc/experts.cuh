@@ -37,6 +37,13 @@ __host__ __device__ inline Plan plan_sections(const int32_t* p, int64_t slots, i
   return v;
 }
 
+// Whether a plan's entry is a place in [0, n); -1 is none, anything else no plan's (reported, not used).
+__device__ __forceinline__ bool plan_place(int64_t v, int64_t n) {
+  if (static_cast<uint64_t>(v) < static_cast<uint64_t>(n)) return true;
+  if (v != -1) set_status(kStatusInvalidArg);
+  return false;
+}
+
 // Loads of what an earlier kernel may have written. These kernels begin while that kernel still runs
 // and wait for it (griddepcontrol.wait); a non-coherent load, or a plain one through a pointer to
 // const that is __restrict__, counts as constant for the whole kernel and could be moved before
@@ -290,7 +297,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_dispatch(const __nv_bfloat16* 
     const int mine = lane < nj ? p.row_of_slot[t * k + j0 + lane] : -1;
     for (int j = 0; j < nj; ++j) {
       const int64_t row = __shfl_sync(0xFFFFFFFFu, mine, j);
-      if (row < 0) continue;
+      if (!plan_place(row, tokens * k)) continue;
       uint4* dst = reinterpret_cast<uint4*>(rows + row * ldr);
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -338,7 +345,7 @@ __global__ void __launch_bounds__(kMoveThreads)
     for (int j = 0; j < nj; ++j) {
       const int64_t row = __shfl_sync(0xFFFFFFFFu, mine, j);
       const float w = __shfl_sync(0xFFFFFFFFu, wmine, j);
-      if (row < 0) continue;
+      if (!plan_place(row, tokens * k)) continue;
       const __nv_bfloat16* src = rows + row * ldr;
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(kMoveThreads)
   if (s >= tokens * k) return;
   const int64_t t = s / k, j = s - t * k;
   const int64_t row = p.row_of_slot[s];
-  if (row < 0) {
+  if (!plan_place(row, tokens * k)) {
     if (lane == 0) d_w[t * lddw + j] = 0.0f;
     return;
   }
@@ -426,6 +433,7 @@ struct QuantExpertsArgs {
   const __nv_bfloat16* x;  // tokens [T, K], or gate|up [S, 2 K]
   int64_t ldx;
   int64_t n;        // tokens, or slots
+  int64_t slots;
   int K, r, kpad;
   int64_t sf_rows;  // rows of the scale layout
   const int32_t* idx;
@@ -497,7 +505,9 @@ __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts(QuantExpert
     dst = sfr = -1;
     if (j0 + lane < nrows) {
       dst = SRC == kQexTokens ? a.p.row_of_slot[src * a.k + j0 + lane] : static_cast<int>(src);
+      if (!plan_place(dst, a.slots)) dst = -1;
       if (dst >= 0) sfr = a.p.sf_row[dst];
+      if (dst >= 0 && !plan_place(sfr, a.sf_rows)) dst = -1;
     }
   };
   // scale byte kb of place m: 8 bytes (a K = 256 pipeline stage of the product) per row and stage

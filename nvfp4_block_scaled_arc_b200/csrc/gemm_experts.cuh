@@ -264,8 +264,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
   pdl_wait();  // the plan and the operands come from earlier kernels
-  for (int e = threadIdx.x; e <= g.experts; e += kGemmThreads) offsets[e] = g.p.offsets[e];
-  __syncthreads();
+  // A buffer that no plan was written to is reported and has no tiles.
+  bool bad = false;
+  for (int e = threadIdx.x; e <= g.experts; e += kGemmThreads) {
+    const int at = g.p.offsets[e], next = g.p.offsets[min(e + 1, g.experts)];
+    offsets[e] = at;
+    bad |= at < 0 || next < at || next > g.slots;
+    if (MX4 && e < g.experts && !bad) {
+      const int blk = g.p.blocks[e];
+      bad |= blk < 0 || 128ll * (blk + static_cast<int64_t>((next - at + 127) / 128)) > g.sfx_rows;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && threadIdx.x == 0) set_status(kStatusInvalidArg);
   if (warp == 2) {
     // first row tile of every expert: exclusive sum of ceil(rows / TN)
     int run = 0;
@@ -287,7 +298,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   cluster_sync_all();  // the other CTA's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int ntiles = first[g.experts] * g.tiles_w;
+  const int ntiles = bad ? 0 : first[g.experts] * g.tiles_w;
   auto tile = [&](int t) { return expert_tile(t, first, offsets, g.experts, g.tiles_w, g.group_m); };
 
   if (warp == 0) {

@@ -452,6 +452,7 @@ arc_status quantize_experts(const void* x, int64_t ldx, int64_t K, const int32_t
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.ldx = ldx;
   a.n = SRC == arc::kQexTokens ? tokens : tokens * k;
+  a.slots = tokens * k;
   a.K = static_cast<int>(K);
   a.r = r;
   a.kpad = static_cast<int>(arc_kpad(K + r));

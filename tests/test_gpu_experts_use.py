@@ -314,6 +314,33 @@ def test_outlier_channel_out_of_range_is_reported():
     assert arc.last_device_status() == 0
 
 
+@pytest.mark.parametrize("fill", [0x7F7F7F7F, -5, 33])
+def test_a_buffer_without_a_plan_is_reported(fill):
+    # the kernels check a plan's entries against their buffers: nothing is written outside (canaries
+    # above), outputs that depend on a place stay as they were
+    T, k, E, K, N = 16, 2, 4, 64, 64
+    plan = arc.ExpertPlan(torch.full((2 * 64 + 3 * 64,), fill, dtype=torch.int32, device="cuda"), T, k, E)
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    rows = torch.zeros(T * k, K, dtype=torch.bfloat16, device="cuda")
+    w16, wt = torch.zeros(E, N, K, dtype=torch.bfloat16, device="cuda"), torch.ones(T, k, device="cuda")
+    w = arc.pack_weight_experts_mxfp4(w16)
+    full, y = _guarded(T * k * N * 2)
+    y = y.view(torch.bfloat16).view(T * k, N)
+    calls = [lambda: arc.dispatch_experts(x, plan, out=y), lambda: arc.combine_experts(rows, wt, plan),
+             lambda: arc.dispatch_experts_grad(rows, plan),
+             lambda: arc.combine_experts_grad(x, rows, wt, plan, d_rows=y),
+             lambda: arc.quantize_act_experts_mxfp4(x, plan), lambda: arc.gemm_experts_bf16(rows, w16, plan, out=y)]
+    good = arc.quantize_act_experts_mxfp4(x, arc.expert_plan(torch.zeros(T, k, dtype=torch.int32, device="cuda"), E))
+    calls.append(lambda: arc.gemm_experts_mxfp4(good, w, plan, out=y))
+    for i, call in enumerate(calls):
+        call()
+        assert arc.last_device_status() == 1, i  # ARC_ERR_INVALID_ARG
+    arc.quantize_swiglu_experts_mxfp4(torch.zeros(T * k, 2 * K, dtype=torch.bfloat16, device="cuda"), plan)
+    _untouched(full, "outputs")
+    assert (full == CANARY).all()
+    arc.last_device_status()
+
+
 @pytest.mark.slow
 def test_sorted_rows_beyond_2_31_elements():
     T, k, E, d = 70000, 8, 9, 4096  # 2.3e9 elements
