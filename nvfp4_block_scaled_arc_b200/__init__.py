@@ -587,14 +587,24 @@ class ExpertPlan:
         return self.buf[at:at + self.slots]
 
 
-@dataclass
 class ExpertMXFP4:
-    """Sorted rows in MXFP4: codes [S, K_pad/2] u8 and scale bytes whose 128-row blocks begin anew
-    with every expert. k_aug = K + r."""
-    codes: torch.Tensor
-    sf: torch.Tensor
-    rows: int
-    k_aug: int
+    """Sorted rows in MXFP4 in one u8 device buffer: codes [S, K_pad/2] and, from the next multiple of
+    256 bytes on, the scale bytes, whose 128-row blocks begin anew with every expert. k_aug = K + r."""
+
+    __slots__ = ("buf", "rows", "k_aug", "sf_at")
+
+    def __init__(self, buf: torch.Tensor, rows: int, k_aug: int):
+        self.buf, self.rows, self.k_aug = buf, rows, k_aug
+        self.sf_at = (rows * (_pad64(k_aug) // 2) + 255) // 256 * 256
+
+    @property
+    def codes(self) -> torch.Tensor:
+        half = _pad64(self.k_aug) // 2
+        return self.buf[:self.rows * half].view(self.rows, half)
+
+    @property
+    def sf(self) -> torch.Tensor:
+        return self.buf[self.sf_at:]
 
 
 @dataclass
@@ -675,7 +685,7 @@ def expert_plan(ids: torch.Tensor, experts: int, out: ExpertPlan | None = None, 
     ld = _rows_of(fn, "ids", ids, dtype, dev, shape)
     if out is None:
         n = 2 * _pad64(experts + 1) + 3 * _pad64(T * k)
-        out = ExpertPlan(torch.empty(n, dtype=_I32, device=ids.device), T, k, experts)
+        out = ExpertPlan(ids.new_empty(n, dtype=_I32), T, k, experts)
     elif (out.tokens, out.k, out.experts) != (T, k, experts):
         raise ValueError("expert_plan: out was made for other sizes")
     _check("arc_expert_plan", lib().arc_expert_plan(
@@ -767,29 +777,27 @@ def _expert_sf_bytes(plan: ExpertPlan, k_aug: int) -> int:
     return (S + 127 * min(plan.experts, S)) // 128 * 1024 * ((_pad64(k_aug) + 255) // 256)
 
 
-def _expert_quantize(fn: str, x: torch.Tensor, plan: ExpertPlan, K: int, idx, out: ExpertMXFP4 | None, stream,
+def _expert_quantize(fn: str, call, x: torch.Tensor, plan: ExpertPlan, K: int, idx, out: ExpertMXFP4 | None, stream,
                      rows: int):
-    dev, S = x.get_device(), plan.tokens * plan.k
+    dev, S = x.get_device(), plan.slots
     r = 0 if idx is None else idx.numel()
     kp = _pad64(K + r)
     if stream is not None or dev < 0 or dev != _device():
         with _on(fn, dev, stream):
-            return _expert_quantize(fn, x, plan, K, idx, out, None, rows)
+            return _expert_quantize(fn, call, x, plan, K, idx, out, None, rows)
     ld = _rows_of(fn, "x" if rows == plan.tokens else "gu", x, _BF16, dev, (rows, x.shape[-1]))
     if idx is not None:
         _flat(fn, "idx", idx, _I32, dev, r)
     nsf = _expert_sf_bytes(plan, K + r)
     if out is None:
-        out = ExpertMXFP4(torch.empty((S, kp // 2), dtype=_U8, device=x.device),
-                          torch.empty(nsf, dtype=_U8, device=x.device), S, K + r)
+        out = ExpertMXFP4(x.new_empty((S * (kp // 2) + 255) // 256 * 256 + nsf, dtype=_U8), S, K + r)
     else:
         if out.rows != S or out.k_aug != K + r:
             raise ValueError(f"{fn}: out was made for other sizes")
-        _flat(fn, "out.codes", out.codes, _U8, dev, S * kp // 2)
-        _flat(fn, "out.sf", out.sf, _U8, dev, nsf)
-    _check("arc_" + fn, getattr(lib(), "arc_" + fn)(
-        x.data_ptr(), ld, K, None if idx is None else idx.data_ptr(), r, _plan_ptr(fn, plan, dev), plan.tokens, plan.k,
-        plan.experts, out.codes.data_ptr(), out.sf.data_ptr(), _raw_stream(dev)))
+        _flat(fn, "out", out.buf, _U8, dev, out.sf_at + nsf)
+    codes = out.buf.data_ptr()
+    _check("arc_" + fn, call(x.data_ptr(), ld, K, None if idx is None else idx.data_ptr(), r, _plan_ptr(fn, plan, dev),
+                             plan.tokens, plan.k, plan.experts, codes, codes + out.sf_at, _raw_stream(dev)))
     return out
 
 
@@ -797,7 +805,8 @@ def quantize_act_experts_mxfp4(x: torch.Tensor, plan: ExpertPlan, idx: torch.Ten
                                out: ExpertMXFP4 | None = None, stream=None) -> ExpertMXFP4:
     """arc_quantize_act_experts_mxfp4: tokens x [T, K] bf16 in MXFP4 with r appended residual channels,
     written to their sorted rows."""
-    return _expert_quantize("quantize_act_experts_mxfp4", x, plan, x.shape[-1], idx, out, stream, plan.tokens)
+    return _expert_quantize("quantize_act_experts_mxfp4", lib().arc_quantize_act_experts_mxfp4, x, plan, x.shape[-1],
+                            idx, out, stream, plan.tokens)
 
 
 def quantize_swiglu_experts_mxfp4(gu: torch.Tensor, plan: ExpertPlan, idx: torch.Tensor | None = None,
@@ -805,7 +814,8 @@ def quantize_swiglu_experts_mxfp4(gu: torch.Tensor, plan: ExpertPlan, idx: torch
     """arc_quantize_swiglu_experts_mxfp4: silu(gate) * up of the sorted rows gu [S, 2F], in MXFP4."""
     if gu.shape[-1] % 2:
         raise ValueError("quantize_swiglu_experts_mxfp4: gu must have as many gate as up columns")
-    return _expert_quantize("quantize_swiglu_experts_mxfp4", gu, plan, gu.shape[-1] // 2, idx, out, stream, plan.slots)
+    return _expert_quantize("quantize_swiglu_experts_mxfp4", lib().arc_quantize_swiglu_experts_mxfp4, gu, plan,
+                            gu.shape[-1] // 2, idx, out, stream, plan.slots)
 
 
 def _expert_weight_ld(fn: str, w: torch.Tensor, dev: int, E: int, N: int, K: int) -> int:
@@ -850,23 +860,23 @@ def pack_weight_experts_mxfp4(w: torch.Tensor, idx: torch.Tensor | None = None, 
 def gemm_experts_mxfp4(a: ExpertMXFP4, w: ExpertWeightMXFP4, plan: ExpertPlan, out: torch.Tensor | None = None,
                        stream=None) -> torch.Tensor:
     """arc_gemm_experts_mxfp4: Y [S, N] bf16 = each sorted row times its expert's weights."""
-    fn, dev, S, n, ka = "gemm_experts_mxfp4", a.codes.get_device(), plan.tokens * plan.k, w.n, a.k_aug
+    fn, dev, S, n, ka = "gemm_experts_mxfp4", a.buf.get_device(), plan.slots, w.n, a.k_aug
     if ka != w.k_aug or w.experts != plan.experts or a.rows != S:
         raise ValueError("gemm_experts_mxfp4: operands of other sizes than the plan's, or of two depths")
     kp = _pad64(ka)
     if stream is not None or dev < 0 or dev != _device():
         with _on(fn, dev, stream):
             return gemm_experts_mxfp4(a, w, plan, out)
-    _flat(fn, "a.codes", a.codes, _U8, dev, S * kp // 2)
-    _flat(fn, "a.sf", a.sf, _U8, dev, _expert_sf_bytes(plan, ka))
+    _flat(fn, "a", a.buf, _U8, dev, a.sf_at + _expert_sf_bytes(plan, ka))
     _flat(fn, "w.codes", w.codes, _U8, dev, w.experts * n * kp // 2)
     _flat(fn, "w.sf", w.sf, _U8, dev, w.experts * ((n + 127) // 128) * ((kp + 127) // 128) * 512)
     if out is None:
-        out, ld_out = torch.empty((S, n), dtype=_BF16, device=a.codes.device), n
+        out, ld_out = a.buf.new_empty((S, n), dtype=_BF16), n
     else:
         ld_out = _rows_of(fn, "out", out, _BF16, dev, (S, n))
+    codes = a.buf.data_ptr()
     _check("arc_gemm_experts_mxfp4", lib().arc_gemm_experts_mxfp4(
-        a.codes.data_ptr(), a.sf.data_ptr(), w.codes.data_ptr(), w.sf.data_ptr(), _plan_ptr(fn, plan, dev), plan.tokens,
+        codes, codes + a.sf_at, w.codes.data_ptr(), w.sf.data_ptr(), _plan_ptr(fn, plan, dev), plan.tokens,
         plan.k, plan.experts, n, ka, out.data_ptr(), ld_out, _raw_stream(dev)))
     return out
 

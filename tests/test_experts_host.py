@@ -115,7 +115,7 @@ def test_binding_refuses_cpu_tensors_and_wrong_plans():
              lambda: arc.quantize_swiglu_experts_mxfp4(rows, plan),
              lambda: arc.pack_weight_experts_mxfp4(torch.zeros(8, 64, 64, dtype=torch.bfloat16)),
              lambda: arc.gemm_experts_bf16(rows, torch.zeros(8, 64, 64, dtype=torch.bfloat16), plan),
-             lambda: arc.gemm_experts_mxfp4(arc.ExpertMXFP4(torch.zeros(64, 32, dtype=torch.uint8), buf, 64, 64),
+             lambda: arc.gemm_experts_mxfp4(arc.ExpertMXFP4(torch.zeros(1 << 16, dtype=torch.uint8), 64, 64),
                                             arc.ExpertWeightMXFP4(buf, buf, 8, 64, 64), plan)]
     for call in calls:
         with pytest.raises(ValueError, match="CUDA tensors"):
@@ -127,4 +127,4 @@ def test_binding_refuses_cpu_tensors_and_wrong_plans():
     with pytest.raises(ValueError, match="experts, N, K"):
         arc.gemm_experts_bf16(rows, rows, plan)
     with pytest.raises(ValueError, match="depths"):
-        arc.gemm_experts_mxfp4(arc.ExpertMXFP4(buf, buf, 64, 64), arc.ExpertWeightMXFP4(buf, buf, 8, 64, 128), plan)
+        arc.gemm_experts_mxfp4(arc.ExpertMXFP4(buf, 64, 64), arc.ExpertWeightMXFP4(buf, buf, 8, 64, 128), plan)

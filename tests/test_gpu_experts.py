@@ -220,9 +220,11 @@ def _check_coded(q, p, codes_ref, sc_ref, k_aug):
 
 
 def _coded_out(plan, k_aug):
-    n = arc.lib().arc_expert_sf_bytes(plan.tokens, plan.k, plan.experts, k_aug)
-    return arc.ExpertMXFP4(torch.full((plan.slots, O.kpad(k_aug) // 2), 0xA5, dtype=torch.uint8, device="cuda"),
-                           torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda"), plan.slots, k_aug)
+    at = (plan.slots * O.kpad(k_aug) // 2 + 255) // 256 * 256
+    n = at + arc.lib().arc_expert_sf_bytes(plan.tokens, plan.k, plan.experts, k_aug)
+    out = arc.ExpertMXFP4(torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda"), plan.slots, k_aug)
+    assert out.sf_at == at
+    return out
 
 
 QUANTS = [(1, 8, 16, 64, 0, "skewed"), (1, 2, 4, 4096, 64, "skewed"), (37, 3, 5, 96, 32, "drop"),
@@ -466,9 +468,10 @@ def test_gpu_refusals():
         lambda: arc.combine_experts_grad(rows, rows, wt, plan), lambda: arc.combine_experts(rows, wt.cpu(), plan),
         lambda: arc.quantize_act_experts_mxfp4(rows, plan), lambda: arc.quantize_swiglu_experts_mxfp4(x, plan),
         lambda: arc.quantize_act_experts_mxfp4(x, plan, torch.arange(32, device="cuda")),
-        lambda: arc.quantize_act_experts_mxfp4(x, plan, out=arc.ExpertMXFP4(a.codes, a.sf[:-1], 8, 64)),
+        lambda: arc.quantize_act_experts_mxfp4(x, plan, out=arc.ExpertMXFP4(a.buf[:-1], 8, 64)),
         lambda: arc.gemm_experts_bf16(rows, w[:2], plan), lambda: arc.gemm_experts_bf16(rows, w[:, :, :32], plan),
         lambda: arc.gemm_experts_bf16(rows, torch.zeros(6, 64, 64, dtype=torch.bfloat16, device="cuda")[::2], plan),
+        lambda: arc.gemm_experts_mxfp4(arc.ExpertMXFP4(a.buf[:-1], 8, 64), q, plan),
         lambda: arc.gemm_experts_mxfp4(a, arc.ExpertWeightMXFP4(q.codes[:-1], q.sf, 3, 64, 64), plan),
         lambda: arc.gemm_experts_mxfp4(a, arc.ExpertWeightMXFP4(q.codes, q.sf[:-1], 3, 64, 64), plan),
         lambda: arc.expert_plan(torch.zeros(4, 2, dtype=torch.int32, device="cuda"), 4, out=plan)]

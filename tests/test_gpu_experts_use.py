@@ -259,8 +259,8 @@ def test_only_the_outputs_are_written(T, k, E, K, N, r, how):
     arc.combine_experts_grad(x, rows, weights, plan, d_rows=mat(S, K), d_weights=mat(T, k, torch.float32))
     for q, src in ((arc.quantize_act_experts_mxfp4, x), (arc.quantize_swiglu_experts_mxfp4, gu)):
         kp = (K + r + 63) // 64 * 64
-        codes, sf = mat(S, kp // 2, torch.uint8), mat(1, arc.lib().arc_expert_sf_bytes(T, k, E, K + r), torch.uint8)
-        a = q(src, plan, idx, out=arc.ExpertMXFP4(codes, sf.view(-1), S, K + r))
+        n = (S * kp // 2 + 255) // 256 * 256 + arc.lib().arc_expert_sf_bytes(T, k, E, K + r)
+        a = q(src, plan, idx, out=arc.ExpertMXFP4(mat(1, n, torch.uint8).view(-1), S, K + r))
     kp = (K + r + 63) // 64 * 64
     wc, ws = mat(E * N, kp // 2, torch.uint8), mat(1, E * arc.mxfp4_sf_bytes(N, K + r), torch.uint8)
     wq = arc.pack_weight_experts_mxfp4(w, idx, out=arc.ExpertWeightMXFP4(wc, ws.view(-1), E, N, K + r))
