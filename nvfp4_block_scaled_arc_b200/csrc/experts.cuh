@@ -270,38 +270,57 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------------------
-// Sorted rows and back. A warp takes one token and a segment of 32 * U 16-byte vectors of it; lane
-// j holds the place (and weight) of choice j, broadcast by shuffle.
+// Sorted rows and back. A group of L lanes (a power of two up to the whole warp, so that narrow rows
+// leave no lane idle) takes one token and a segment of L * U 16-byte vectors of it; a lane holds the
+// place (and weight) of one of L choices at a time, broadcast by shuffle. At 2048 columns the rows
+// move at 0.93 to 0.99 of the copy rate; with 8 choices of 256 columns whole warps reached 0.49 (combine)
+// and 0.30 (its gradient), groups 0.80 and 0.83.
 // ---------------------------------------------------------------------------------------------
 
 constexpr int kMoveThreads = 256;
 
+// This lane's group and place in it: t the item, v0 the first vector, false behind the last item.
+struct MoveLane {
+  int64_t t;
+  int l, v0;
+};
 template <int U>
-__global__ void __launch_bounds__(kMoveThreads) k_dispatch(const __nv_bfloat16* x, int64_t ldx, int vecs,
-                                                           Plan p, int64_t tokens, int k,
+__device__ __forceinline__ MoveLane move_lane(int log_lanes, int nseg) {
+  const int lane = threadIdx.x & 31, lanes = 1 << log_lanes;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
+  const int64_t group = (warp << (5 - log_lanes)) + (lane >> log_lanes);
+  MoveLane m;
+  m.t = nseg == 1 ? group : group / nseg;
+  m.l = lane & (lanes - 1);
+  m.v0 = static_cast<int>(group - m.t * nseg) * lanes * U + m.l;
+  return m;
+}
+
+template <int U>
+__global__ void __launch_bounds__(kMoveThreads) k_dispatch(const __nv_bfloat16* x, int64_t ldx, int vecs, int log_lanes,
+                                                           int nseg, Plan p, int64_t tokens, int k,
                                                            __nv_bfloat16* rows, int64_t ldr) {
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int nseg = (vecs + 32 * U - 1) / (32 * U);
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = task / nseg;
+  const int lanes = 1 << log_lanes;
+  const MoveLane m = move_lane<U>(log_lanes, nseg);
+  const bool valid = m.t < tokens;
   pdl_wait();
-  if (t >= tokens) return;
-  const int v0 = static_cast<int>(task - t * nseg) * 32 * U + lane;
   uint4 w[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    w[u] = v0 + 32 * u < vecs ? ld_v4_once(x + t * ldx + 8 * (v0 + 32 * u)) : make_uint4(0, 0, 0, 0);
-  for (int j0 = 0; j0 < k; j0 += 32) {
-    const int nj = min(32, k - j0);
-    const int mine = lane < nj ? p.row_of_slot[t * k + j0 + lane] : -1;
+  for (int u = 0; u < U; ++u) {
+    const int v = m.v0 + lanes * u;
+    w[u] = valid && v < vecs ? ld_v4_once(x + m.t * ldx + 8 * v) : make_uint4(0, 0, 0, 0);
+  }
+  for (int j0 = 0; j0 < k; j0 += lanes) {
+    const int nj = min(lanes, k - j0);
+    const int mine = valid && m.l < nj ? p.row_of_slot[m.t * k + j0 + m.l] : -1;
     for (int j = 0; j < nj; ++j) {
-      const int64_t row = __shfl_sync(0xFFFFFFFFu, mine, j);
+      const int64_t row = __shfl_sync(0xFFFFFFFFu, mine, j, lanes);
       if (!plan_place(row, tokens * k)) continue;
       uint4* dst = reinterpret_cast<uint4*>(rows + row * ldr);
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (v0 + 32 * u < vecs) dst[v0 + 32 * u] = w[u];
+        if (m.v0 + lanes * u < vecs) dst[m.v0 + lanes * u] = w[u];
     }
   }
 }
@@ -318,104 +337,133 @@ __device__ __forceinline__ void fma_bf16x8(float (&acc)[8], float w, uint4 v) {
 }
 
 // y[t] = bf16( sum_j w_j rows[row_j] [+ add] ): the combine, and with weights of one (weights ==
-// nullptr) the gradient of the dispatch.
-template <int U>
+// nullptr) the gradient of the dispatch. WHOLE: a group is the warp (16384 tokens of 2 x 4096: 64 us,
+// against 73 us without that branch taken for the warp as a whole). Otherwise several choices'
+// vectors are requested before the first is added (32768 tokens of 8 x 128: 15 against 45 us for a
+// warp per token).
+template <int U, bool WHOLE>
 __global__ void __launch_bounds__(kMoveThreads)
-    k_combine(const __nv_bfloat16* rows, int64_t ldr, int vecs, const float* weights,
+    k_combine(const __nv_bfloat16* rows, int64_t ldr, int vecs, int log_lanes, int nseg, const float* weights,
               int64_t ldw, Plan p, int64_t tokens, int k, const __nv_bfloat16* add, int64_t lda, __nv_bfloat16* y,
               int64_t ldy) {
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int nseg = (vecs + 32 * U - 1) / (32 * U);
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = task / nseg;
+  const int lanes = WHOLE ? 32 : 1 << log_lanes;
+  const MoveLane m = move_lane<U>(WHOLE ? 5 : log_lanes, nseg);
+  const bool valid = m.t < tokens;
   pdl_wait();
-  if (t >= tokens) return;
-  const int v0 = static_cast<int>(task - t * nseg) * 32 * U + lane;
+  if (WHOLE && !valid) return;
   float acc[U][8];
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[u][i] = 0.0f;
-  for (int j0 = 0; j0 < k; j0 += 32) {
-    const int nj = min(32, k - j0);
-    const int mine = lane < nj ? p.row_of_slot[t * k + j0 + lane] : -1;
-    const float wmine = weights != nullptr && lane < nj ? weights[t * ldw + j0 + lane] : 1.0f;
+  for (int j0 = 0; j0 < k; j0 += lanes) {
+    const int nj = min(lanes, k - j0);
+    const bool has = valid && m.l < nj;
+    const int mine = has ? p.row_of_slot[m.t * k + j0 + m.l] : -1;
+    const float wmine = has && weights != nullptr ? weights[m.t * ldw + j0 + m.l] : 1.0f;
+    if constexpr (WHOLE) {
 #pragma unroll 4
-    for (int j = 0; j < nj; ++j) {
-      const int64_t row = __shfl_sync(0xFFFFFFFFu, mine, j);
-      const float w = __shfl_sync(0xFFFFFFFFu, wmine, j);
-      if (!plan_place(row, tokens * k)) continue;
-      const __nv_bfloat16* src = rows + row * ldr;
+      for (int j = 0; j < nj; ++j) {
+        const int64_t row = __shfl_sync(0xFFFFFFFFu, mine, j);
+        const float w = __shfl_sync(0xFFFFFFFFu, wmine, j);
+        if (!plan_place(row, tokens * k)) continue;
+        const __nv_bfloat16* src = rows + row * ldr;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (v0 + 32 * u < vecs) fma_bf16x8(acc[u], w, ld_v4_once(src + 8 * (v0 + 32 * u)));
+        for (int u = 0; u < U; ++u)
+          if (m.v0 + 32 * u < vecs) fma_bf16x8(acc[u], w, ld_v4_once(src + 8 * (m.v0 + 32 * u)));
+      }
+      continue;
+    }
+    // a choice without a row adds 0 * 0
+    constexpr int J = U == 4 ? 2 : 4;
+    for (int j = 0; j < nj; j += J) {
+      uint4 v[J][U];
+      float w[J];
+#pragma unroll
+      for (int i = 0; i < J; ++i) {
+        const int64_t row = __shfl_sync(0xFFFFFFFFu, mine, j + i, lanes);
+        w[i] = __shfl_sync(0xFFFFFFFFu, wmine, j + i, lanes);
+        const bool ok = j + i < nj && plan_place(row, tokens * k);
+        if (!ok) w[i] = 0.0f;
+        const __nv_bfloat16* src = rows + row * ldr + 8 * m.v0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          v[i][u] = make_uint4(0, 0, 0, 0);
+          if (ok && m.v0 + lanes * u < vecs) v[i][u] = ld_v4_once(src + 8 * lanes * u);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < J; ++i)
+#pragma unroll
+        for (int u = 0; u < U; ++u) fma_bf16x8(acc[u], w[i], v[i][u]);
     }
   }
+  if (!valid) return;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int v = v0 + 32 * u;
+    const int v = m.v0 + lanes * u;
     if (v >= vecs) continue;
     if (add != nullptr)
-      fma_bf16x8(acc[u], 1.0f, *reinterpret_cast<const uint4*>(add + t * lda + 8 * v));
-    *reinterpret_cast<uint4*>(y + t * ldy + 8 * v) =
+      fma_bf16x8(acc[u], 1.0f, *reinterpret_cast<const uint4*>(add + m.t * lda + 8 * v));
+    *reinterpret_cast<uint4*>(y + m.t * ldy + 8 * v) =
         make_uint4(pack_bf16x2_rn(acc[u][0], acc[u][1]), pack_bf16x2_rn(acc[u][2], acc[u][3]),
                    pack_bf16x2_rn(acc[u][4], acc[u][5]), pack_bf16x2_rn(acc[u][6], acc[u][7]));
   }
 }
 
-// One warp per slot: d_rows[row] = bf16(w d_y[t]) and d_w = <d_y[t], rows[row]> (fp32 partial sums
+// One group per slot: d_rows[row] = bf16(w d_y[t]) and d_w = <d_y[t], rows[row]> (fp32 partial sums
 // by lane, joined by shuffles: a fixed order). d_rows may be rows: each vector is read before the
 // same lane writes it.
 __global__ void __launch_bounds__(kMoveThreads)
-    k_combine_grad(const __nv_bfloat16* dy, int64_t lddy, const __nv_bfloat16* rows, int64_t ldr,
-                   int vecs, const float* weights, int64_t ldw, Plan p, int64_t tokens, int k,
+    k_combine_grad(const __nv_bfloat16* dy, int64_t lddy, const __nv_bfloat16* rows, int64_t ldr, int vecs,
+                   int log_lanes, const float* weights, int64_t ldw, Plan p, int64_t tokens, int k,
                    __nv_bfloat16* d_rows, int64_t lddr, float* d_w, int64_t lddw) {
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t s = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
+  const int lanes = 1 << log_lanes;
+  const MoveLane m = move_lane<1>(log_lanes, 1);
+  const int64_t s = m.t, slots = tokens * k;
   pdl_wait();
-  if (s >= tokens * k) return;
-  const int64_t t = s / k, j = s - t * k;
-  const int64_t row = p.row_of_slot[s];
-  if (!plan_place(row, tokens * k)) {
-    if (lane == 0) d_w[t * lddw + j] = 0.0f;
-    return;
-  }
-  const float w = weights[t * ldw + j];
-  const __nv_bfloat16* a = dy + t * lddy;
-  const __nv_bfloat16* b = rows + row * ldr;
-  uint4* dst = reinterpret_cast<uint4*>(d_rows + row * lddr);
+  const bool valid = s < slots;
+  const int64_t t = valid ? s / k : 0, j = s - t * k;
+  const int64_t row = valid ? p.row_of_slot[s] : -1;
+  const bool has = plan_place(row, slots);
   float dot = 0.0f;
-  constexpr int U = 4;  // vectors in flight: all loaded before the first is written (rows may be d_rows)
-  for (int v0 = lane; v0 < vecs; v0 += 32 * U) {
-    uint4 g[U], r[U];
+  if (has) {
+    const float w = weights[t * ldw + j];
+    const __nv_bfloat16* a = dy + t * lddy;
+    const __nv_bfloat16* b = rows + row * ldr;
+    uint4* dst = reinterpret_cast<uint4*>(d_rows + row * lddr);
+    constexpr int U = 4;  // vectors in flight: all loaded before the first is written (rows may be d_rows)
+    for (int v0 = m.l; v0 < vecs; v0 += lanes * U) {
+      uint4 g[U], r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int v = v0 + 32 * u;
-      g[u] = r[u] = make_uint4(0, 0, 0, 0);
-      if (v < vecs) {
-        g[u] = ld_v4(a + 8 * v);
-        r[u] = *reinterpret_cast<const uint4*>(b + 8 * v);
+      for (int u = 0; u < U; ++u) {
+        const int v = v0 + lanes * u;
+        g[u] = r[u] = make_uint4(0, 0, 0, 0);
+        if (v < vecs) {
+          g[u] = ld_v4(a + 8 * v);
+          r[u] = *reinterpret_cast<const uint4*>(b + 8 * v);
+        }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t gs[4] = {g[u].x, g[u].y, g[u].z, g[u].w}, rs[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
-      uint32_t o[4];
+      for (int u = 0; u < U; ++u) {
+        const uint32_t gs[4] = {g[u].x, g[u].y, g[u].z, g[u].w}, rs[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
+        uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float g0 = bf16_lo(gs[i]), g1 = bf16_hi(gs[i]);
-        dot = __fmaf_rn(g0, bf16_lo(rs[i]), dot);
-        dot = __fmaf_rn(g1, bf16_hi(rs[i]), dot);
-        o[i] = pack_bf16x2_rn(__fmul_rn(w, g0), __fmul_rn(w, g1));
+        for (int i = 0; i < 4; ++i) {
+          const float g0 = bf16_lo(gs[i]), g1 = bf16_hi(gs[i]);
+          dot = __fmaf_rn(g0, bf16_lo(rs[i]), dot);
+          dot = __fmaf_rn(g1, bf16_hi(rs[i]), dot);
+          o[i] = pack_bf16x2_rn(__fmul_rn(w, g0), __fmul_rn(w, g1));
+        }
+        if (v0 + lanes * u < vecs) dst[v0 + lanes * u] = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      if (v0 + 32 * u < vecs) dst[v0 + 32 * u] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-  if (lane == 0) d_w[t * lddw + j] = dot;
+  __syncwarp();
+  for (int o = lanes >> 1; o; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+  if (valid && m.l == 0) d_w[t * lddw + j] = dot;
 }
 
 // ---------------------------------------------------------------------------------------------

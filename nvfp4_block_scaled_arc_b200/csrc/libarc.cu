@@ -414,14 +414,26 @@ arc_status launch_pdl(void (*kern)(P...), int64_t grid, int block, size_t smem, 
   return ARC_ERR_CUDA;
 }
 
-// 16-byte vectors per lane of the move kernels: four where that still fills the machine (16384 tokens
-// of 2 x 4096: 68 against 86 us), one where a few tokens are spread over more warps.
-int move_unroll(int64_t tokens, int64_t vecs) { return tokens * ((vecs + 127) / 128) >= 148 * 32 ? 4 : 1; }
-
-// CTAs of the move kernels: a warp per (token, segment of 32 u vectors).
-int64_t move_blocks(int64_t tokens, int64_t vecs, int u) {
-  const int64_t tasks = tokens * ((vecs + 32 * u - 1) / (32 * u));
-  return (tasks + arc::kMoveThreads / 32 - 1) / (arc::kMoveThreads / 32);
+// Shape of a move kernel's grid: U 16-byte vectors per lane, groups of 2^log_lanes lanes, nseg
+// segments of a row. Four vectors per lane where that still fills the machine (16384 tokens of 2 x
+// 4096: 68 against 86 us), one where a few tokens are spread over more warps.
+struct MoveShape {
+  int u, log_lanes, nseg;
+  int64_t blocks;
+};
+MoveShape move_shape(int64_t items, int64_t vecs, int u) {
+  MoveShape m;
+  m.u = u;
+  m.log_lanes = 0;
+  while (m.log_lanes < 5 && (static_cast<int64_t>(u) << m.log_lanes) < vecs) ++m.log_lanes;
+  m.nseg = static_cast<int>((vecs + (u << m.log_lanes) - 1) / (u << m.log_lanes));
+  const int64_t groups = items * m.nseg, per_block = static_cast<int64_t>(arc::kMoveThreads) >> m.log_lanes;
+  m.blocks = (groups + per_block - 1) / per_block;
+  return m;
+}
+MoveShape move_shape(int64_t tokens, int64_t vecs) {
+  const MoveShape four = move_shape(tokens, vecs, 4);
+  return four.blocks * (arc::kMoveThreads / 32) >= 148 * 32 ? four : move_shape(tokens, vecs, 1);
 }
 
 arc_status move_check(int64_t d, int64_t ld_a, int64_t ld_b, const void* a, const void* b, const int32_t* plan,
@@ -805,11 +817,11 @@ arc_status arc_dispatch_experts_bf16(const void* x_bf16, int64_t ldx, int64_t d,
   arc_status st = move_check(d, ldx, ld_rows, x_bf16, rows_bf16, plan, tokens, k, experts);
   if (st != ARC_OK) return st;
   if ((st = device_check(nullptr)) != ARC_OK) return st;
-  const int u = move_unroll(tokens, d / 8);
-  return launch_pdl(u == 4 ? arc::k_dispatch<4> : arc::k_dispatch<1>, move_blocks(tokens, d / 8, u),
-                    arc::kMoveThreads, 0, 1, S(stream), static_cast<const __nv_bfloat16*>(x_bf16), ldx,
-                    static_cast<int>(d / 8), arc::plan_sections(plan, tokens * k, experts), tokens, k,
-                    static_cast<__nv_bfloat16*>(rows_bf16), ld_rows);
+  const MoveShape m = move_shape(tokens, d / 8);
+  return launch_pdl(m.u == 4 ? arc::k_dispatch<4> : arc::k_dispatch<1>, m.blocks, arc::kMoveThreads, 0, 1, S(stream),
+                    static_cast<const __nv_bfloat16*>(x_bf16), ldx, static_cast<int>(d / 8), m.log_lanes, m.nseg,
+                    arc::plan_sections(plan, tokens * k, experts), tokens, k, static_cast<__nv_bfloat16*>(rows_bf16),
+                    ld_rows);
 }
 
 static arc_status combine_rows(const void* rows, int64_t ld_rows, int64_t d, const float* weights, int64_t ld_weights,
@@ -817,12 +829,12 @@ static arc_status combine_rows(const void* rows, int64_t ld_rows, int64_t d, con
                                int64_t ld_add, void* y, int64_t ldy, arc_stream_t stream) {
   arc_status st = device_check(nullptr);
   if (st != ARC_OK) return st;
-  const int u = move_unroll(tokens, d / 8);
-  return launch_pdl(u == 4 ? arc::k_combine<4> : arc::k_combine<1>, move_blocks(tokens, d / 8, u),
-                    arc::kMoveThreads, 0, 1, S(stream), static_cast<const __nv_bfloat16*>(rows), ld_rows,
-                    static_cast<int>(d / 8), weights, ld_weights,
-                    arc::plan_sections(plan, tokens * k, experts), tokens, k, static_cast<const __nv_bfloat16*>(add),
-                    ld_add, static_cast<__nv_bfloat16*>(y), ldy);
+  const MoveShape m = move_shape(tokens, d / 8);
+  const auto kern = m.log_lanes == 5 ? (m.u == 4 ? arc::k_combine<4, true> : arc::k_combine<1, true>)
+                                     : (m.u == 4 ? arc::k_combine<4, false> : arc::k_combine<1, false>);
+  return launch_pdl(kern, m.blocks, arc::kMoveThreads, 0, 1, S(stream), static_cast<const __nv_bfloat16*>(rows),
+                    ld_rows, static_cast<int>(d / 8), m.log_lanes, m.nseg, weights, ld_weights, arc::plan_sections(plan, tokens * k, experts), tokens, k,
+                    static_cast<const __nv_bfloat16*>(add), ld_add, static_cast<__nv_bfloat16*>(y), ldy);
 }
 
 arc_status arc_dispatch_experts_grad_bf16(const void* d_rows_bf16, int64_t ld_rows, int64_t d, const int32_t* plan,
@@ -858,10 +870,10 @@ arc_status arc_combine_experts_grad_bf16(const void* d_y_bf16, int64_t ld_dy, co
     return ARC_ERR_ALIGNMENT;
   if ((st = device_check(nullptr)) != ARC_OK) return st;
   const int64_t slots = tokens * k;
-  return launch_pdl(arc::k_combine_grad, (slots + arc::kMoveThreads / 32 - 1) / (arc::kMoveThreads / 32),
-                    arc::kMoveThreads, 0, 1, S(stream), static_cast<const __nv_bfloat16*>(d_y_bf16), ld_dy,
-                    static_cast<const __nv_bfloat16*>(rows_bf16), ld_rows, static_cast<int>(d / 8), weights,
-                    ld_weights, arc::plan_sections(plan, slots, experts), tokens, k,
+  const MoveShape m = move_shape(slots, std::min<int64_t>(d / 8, 128), 4);  // one group per slot
+  return launch_pdl(arc::k_combine_grad, m.blocks, arc::kMoveThreads, 0, 1, S(stream),
+                    static_cast<const __nv_bfloat16*>(d_y_bf16), ld_dy, static_cast<const __nv_bfloat16*>(rows_bf16),
+                    ld_rows, static_cast<int>(d / 8), m.log_lanes, weights, ld_weights, arc::plan_sections(plan, slots, experts), tokens, k,
                     static_cast<__nv_bfloat16*>(d_rows_bf16), ld_drows, d_weights, ld_dw);
 }
 
