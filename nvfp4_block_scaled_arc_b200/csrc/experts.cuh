@@ -470,9 +470,9 @@ __global__ void __launch_bounds__(kMoveThreads)
 // MXFP4 quantization into sorted order (format and arithmetic of k_quant_mx_rows). SRC tokens: the
 // row of a token is coded once and written to the token's k sorted rows. SRC SwiGLU: row i of
 // gate|up gives act = bf16(silu(gate) * up), coded into sorted row i; act never goes to memory. A
-// CTA takes one source row, a lane one block of 32 values (one 16-byte store of codes for each
-// destination). The row's scale bytes stay in shared memory for the appended blocks of 32 outlier
-// channels, a lane each, whose values are read again (two bytes, or a gate and an up).
+// lane takes one block of 32 values (one 16-byte store of codes for each destination). The row's
+// scale bytes stay in shared memory for the appended blocks of 32 outlier channels, a lane each,
+// whose values are read again (two bytes, or a gate and an up).
 // ---------------------------------------------------------------------------------------------
 
 constexpr int kQexTokens = 0, kQexSwiglu = 1;
@@ -536,32 +536,110 @@ __device__ __forceinline__ void load_block(const __nv_bfloat16* row, int K, int 
 
 constexpr int kQexMaxWarps = 8;
 
+// Four lanes' scale bytes as one 32-bit word, in every fourth lane.
+__device__ __forceinline__ uint32_t join_scales(uint32_t sb) {
+  sb |= __shfl_down_sync(0xFFFFFFFFu, sb, 1) << 8;
+  return sb | __shfl_down_sync(0xFFFFFFFFu, sb, 2) << 16;
+}
+
+// The block of 32 values w coded: its scale byte, codes, and whether it is all zero.
+__device__ __forceinline__ uint4 code_block(const uint32_t (&w)[16], uint32_t& sb, bool& zero) {
+  uint32_t mw = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) mw = __vmaxu2(mw, w[i] & 0x7FFF7FFFu);
+  const uint32_t am = max(mw & 0xFFFFu, mw >> 16) << 16;
+  sb = mx_scale_byte(am);
+  zero = am == 0u;
+  if (zero) return make_uint4(0u, 0u, 0u, 0u);
+  const float inv = mx_inv_scale(sb);
+  uint64_t p[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p[e] = f2_pack(bf16_lo(w[e]), bf16_hi(w[e]));
+  const uint2 lo = mx_encode16(p, inv);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p[e] = f2_pack(bf16_lo(w[8 + e]), bf16_hi(w[8 + e]));
+  const uint2 hi = mx_encode16(p, inv);
+  return make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+
+// E2M1 code of one value (round to nearest even, saturating at +-6).
+__device__ __forceinline__ uint32_t e2m1_rn_sat(float v) {
+  uint32_t out;
+  asm("{\n\t.reg .b8 b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+      "cvt.u32.u8 %0, b;\n\t}"
+      : "=r"(out)
+      : "f"(v), "f"(0.0f));
+  return out & 15u;
+}
+
+// Residual of an outlier channel with value bits xw in a block of scale byte t, the code formed
+// again from both.
+__device__ __forceinline__ float outlier_residual(uint32_t xw, uint32_t t) {
+  const float xv = __uint_as_float(xw << 16);
+  if (t == kMxZeroBlock) return xv;
+  return __fsub_rn(xv, __fmul_rn(e2m1_value(e2m1_rn_sat(__fmul_rn(xv, mx_inv_scale(t)))), mx_scale(t)));
+}
+
+// The appended block of the warp's 32 residuals: its scale byte, and eight lanes' codes as one 32-bit
+// word (the first lane's lowest) in every eighth lane.
+__device__ __forceinline__ uint32_t code_residuals(float res, uint32_t& sb) {
+  const uint32_t am = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(res)));
+  sb = mx_scale_byte(am);
+  uint32_t code = am == 0u ? 0u : e2m1_rn_sat(__fmul_rn(res, mx_inv_scale(sb)));
+  code |= __shfl_down_sync(0xFFFFFFFFu, code, 1) << 4;
+  code |= __shfl_down_sync(0xFFFFFFFFu, code, 2) << 8;
+  return code | __shfl_down_sync(0xFFFFFFFFu, code, 4) << 16;
+}
+
+// Scale byte kb of place m: 8 bytes (a K = 256 pipeline stage of the product) per row and stage.
+__device__ __forceinline__ uint8_t* expert_sf_at(const QuantExpertsArgs& a, int64_t m, int kb) {
+  return a.sf + ((kb >> 3) * a.sf_rows + m) * 8 + (kb & 7);
+}
+
+// The j-th destination of source row src: its sorted row and scale place, or -1.
+template <int SRC>
+__device__ __forceinline__ void expert_places(const QuantExpertsArgs& a, int64_t src, int j, int& dst, int& sfr) {
+  dst = SRC == kQexTokens ? a.p.row_of_slot[src * a.k + j] : static_cast<int>(src);
+  sfr = -1;
+  if (!plan_place(dst, a.slots)) dst = -1;
+  if (dst >= 0) sfr = a.p.sf_row[dst];
+  if (dst >= 0 && !plan_place(sfr, a.sf_rows)) dst = -1;
+}
+
+// Stores block b of a row (the coding of it in this lane) to one destination; every lane of the group
+// calls it with its own block, b >= nblk where it has none.
+__device__ __forceinline__ void store_block(const QuantExpertsArgs& a, int64_t dst, int64_t m, int b, int nblk,
+                                            uint4 codes, uint32_t sb, uint32_t joined) {
+  uint8_t* crow = a.codes + dst * (a.kpad >> 1);
+  if (b < nblk) *reinterpret_cast<uint4*>(crow + 16 * b) = codes;
+  if ((b & ~3) + 3 < nblk) {  // the word's four blocks exist
+    if ((b & 3) == 0) *reinterpret_cast<uint32_t*>(expert_sf_at(a, m, b)) = joined;
+  } else if (b < nblk) {
+    *expert_sf_at(a, m, b) = static_cast<uint8_t>(sb);
+  }
+  // the last block's lane also zeroes the block that pads an odd number of blocks to K_pad
+  const int kbz = nblk + (a.r >> 5);
+  if (b == nblk - 1 && 32 * kbz < a.kpad) {
+    *reinterpret_cast<uint4*>(crow + 16 * kbz) = make_uint4(0, 0, 0, 0);
+    *expert_sf_at(a, m, kbz) = 0;
+  }
+}
+
+// A CTA for each row. The row's scale bytes stay in shared memory for the appended blocks.
 template <int SRC>
 __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts(QuantExpertsArgs a) {
-  extern __shared__ uint8_t qex_sb[];  // the row's scale bytes, kMxZeroBlock for an all-zero block
-  pdl_launch_dependents();             // the GEMM that follows may set itself up meanwhile
+  extern __shared__ uint8_t qex_sb[];  // kMxZeroBlock for an all-zero block
+  pdl_launch_dependents();  // the GEMM that follows may set itself up meanwhile
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = static_cast<int>(blockDim.x >> 5);
   const int nblk = a.K >> 5, nres = a.r >> 5;
   const int64_t src = blockIdx.x;
   pdl_wait();
   if (SRC == kQexSwiglu && src >= a.p.offsets[a.experts]) return;
   const __nv_bfloat16* row = a.x + src * a.ldx;
-  const int64_t cpitch = a.kpad >> 1;
   const int nrows = SRC == kQexTokens ? a.k : 1;
-  // lane j: sorted row and scale place of the source row's j-th destination (32 at a time)
-  auto places = [&](int j0, int& dst, int& sfr) {
-    dst = sfr = -1;
-    if (j0 + lane < nrows) {
-      dst = SRC == kQexTokens ? a.p.row_of_slot[src * a.k + j0 + lane] : static_cast<int>(src);
-      if (!plan_place(dst, a.slots)) dst = -1;
-      if (dst >= 0) sfr = a.p.sf_row[dst];
-      if (dst >= 0 && !plan_place(sfr, a.sf_rows)) dst = -1;
-    }
-  };
-  // scale byte kb of place m: 8 bytes (a K = 256 pipeline stage of the product) per row and stage
-  auto sf_at = [&](int64_t m, int kb) { return a.sf + ((kb >> 3) * a.sf_rows + m) * 8 + (kb & 7); };
-  int dst0, sfr0;
-  places(0, dst0, sfr0);
+  int dst0 = -1, sfr0 = -1;  // lane j: the j-th destination (32 at a time)
+  if (lane < nrows) expert_places<SRC>(a, src, lane, dst0, sfr0);
   // the values of the warp's first appended block
   int oc = -1;
   uint32_t og = 0, ou = 0;
@@ -576,97 +654,81 @@ __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts(QuantExpert
     }
   };
   if (warp < nres) outlier(warp);
+  auto each_place = [&](auto&& store) {
+    for (int j0 = 0; j0 < nrows; j0 += 32) {
+      int dsts = dst0, sfrs = sfr0;
+      if (j0) {
+        dsts = -1;
+        if (j0 + lane < nrows) expert_places<SRC>(a, src, j0 + lane, dsts, sfrs);
+      }
+      const int nj = min(32, nrows - j0);
+      for (int j = 0; j < nj; ++j) {
+        const int64_t dst = __shfl_sync(0xFFFFFFFFu, dsts, j), m = __shfl_sync(0xFFFFFFFFu, sfrs, j);
+        if (dst >= 0) store(dst, m);
+      }
+    }
+  };
   for (int b0 = 32 * warp; b0 < nblk; b0 += 32 * nwarps) {
     const int b = b0 + lane;
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = 0u;
     if (b < nblk) load_block<SRC>(row, a.K, 32 * b, w);
-    uint32_t mw = 0u;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) mw = __vmaxu2(mw, w[i] & 0x7FFF7FFFu);
-    const uint32_t am = max(mw & 0xFFFFu, mw >> 16) << 16;
-    const uint32_t sb = mx_scale_byte(am);
-    const float inv = mx_inv_scale(sb);
-    uint4 cc = make_uint4(0u, 0u, 0u, 0u);
-    if (am != 0u) {
-      uint64_t p[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = f2_pack(bf16_lo(w[e]), bf16_hi(w[e]));
-      const uint2 lo = mx_encode16(p, inv);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = f2_pack(bf16_lo(w[8 + e]), bf16_hi(w[8 + e]));
-      const uint2 hi = mx_encode16(p, inv);
-      cc = make_uint4(lo.x, lo.y, hi.x, hi.y);
-    }
-    if (nres > 0 && b < nblk) qex_sb[b] = static_cast<uint8_t>(am == 0u ? kMxZeroBlock : sb);
-    // four lanes' scale bytes make one 32-bit word, in every fourth lane
-    uint32_t sw = sb;
-    sw |= __shfl_down_sync(0xFFFFFFFFu, sw, 1) << 8;
-    sw |= __shfl_down_sync(0xFFFFFFFFu, sw, 2) << 16;
-    const bool whole = (b & ~3) + 3 < nblk;  // the word's four blocks exist
-    // the last lane of the row also zeroes the block that pads an odd number of blocks to K_pad
-    const int kbz = nblk + nres;
-    const bool pad = b == nblk - 1 && 32 * kbz < a.kpad;
-    for (int j0 = 0; j0 < nrows; j0 += 32) {
-      int dsts = dst0, sfrs = sfr0;
-      if (j0) places(j0, dsts, sfrs);
-      const int nj = min(32, nrows - j0);
-      for (int j = 0; j < nj; ++j) {
-        const int64_t dst = __shfl_sync(0xFFFFFFFFu, dsts, j);
-        const int64_t m = __shfl_sync(0xFFFFFFFFu, sfrs, j);
-        if (dst < 0) continue;
-        uint8_t* crow = a.codes + dst * cpitch;
-        if (b < nblk) *reinterpret_cast<uint4*>(crow + 16 * b) = cc;
-        if (whole) {
-          if ((lane & 3) == 0) *reinterpret_cast<uint32_t*>(sf_at(m, b)) = sw;
-        } else if (b < nblk) {
-          *sf_at(m, b) = static_cast<uint8_t>(sb);
-        }
-        if (pad) {
-          *reinterpret_cast<uint4*>(crow + 16 * kbz) = make_uint4(0, 0, 0, 0);
-          *sf_at(m, kbz) = 0;
-        }
-      }
-    }
+    uint32_t sb;
+    bool zero;
+    const uint4 cc = code_block(w, sb, zero);
+    if (nres > 0 && b < nblk) qex_sb[b] = static_cast<uint8_t>(zero ? kMxZeroBlock : sb);
+    const uint32_t joined = join_scales(sb);
+    each_place([&](int64_t dst, int64_t m) { store_block(a, dst, m, b, nblk, cc, sb, joined); });
   }
   if (nres == 0) return;
   __syncthreads();
   for (int rb = warp; rb < nres; rb += nwarps) {
-    // ---- outlier channels: x - E2M1(code) * X, the code formed again from x and the block's byte
     if (rb != warp) outlier(rb);
     float res = 0.0f;
-    if (oc >= 0) {
-      const uint32_t xw = SRC == kQexSwiglu ? silu_mul_pair(og, ou) & 0xFFFFu : og;
-      const float xv = __uint_as_float(xw << 16);
-      const uint32_t t = qex_sb[oc >> 5];
-      res = xv;
-      if (t != kMxZeroBlock) {
-        float q[8] = {__fmul_rn(xv, mx_inv_scale(t)), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        res = __fsub_rn(xv, __fmul_rn(e2m1_value(e2m1x8_rn_sat(q) & 15u), mx_scale(t)));
-      }
-    }
-    const uint32_t am = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(res)));
-    const uint32_t sb = mx_scale_byte(am);
-    float q[8] = {__fmul_rn(res, mx_inv_scale(sb)), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    uint32_t code = am == 0u ? 0u : e2m1x8_rn_sat(q) & 15u;
-    // eight lanes' codes make one 32-bit word, the first lane's lowest
-    code |= __shfl_down_sync(0xFFFFFFFFu, code, 1) << 4;
-    code |= __shfl_down_sync(0xFFFFFFFFu, code, 2) << 8;
-    code |= __shfl_down_sync(0xFFFFFFFFu, code, 4) << 16;
+    if (oc >= 0) res = outlier_residual(SRC == kQexSwiglu ? silu_mul_pair(og, ou) & 0xFFFFu : og, qex_sb[oc >> 5]);
+    uint32_t sb;
+    const uint32_t code = code_residuals(res, sb);
     const int kb = nblk + rb;
-    for (int j0 = 0; j0 < nrows; j0 += 32) {
-      int dsts = dst0, sfrs = sfr0;
-      if (j0) places(j0, dsts, sfrs);
-      const int nj = min(32, nrows - j0);
-      for (int j = 0; j < nj; ++j) {
-        const int64_t dst = __shfl_sync(0xFFFFFFFFu, dsts, j);
-        const int64_t m = __shfl_sync(0xFFFFFFFFu, sfrs, j);
-        if (dst < 0) continue;
-        if ((lane & 7) == 0)
-          *reinterpret_cast<uint32_t*>(a.codes + dst * cpitch + 16 * kb + (lane >> 1)) = code;
-        if (lane == 1) *sf_at(m, kb) = static_cast<uint8_t>(sb);
-      }
+    each_place([&](int64_t dst, int64_t m) {
+      if ((lane & 7) == 0)
+        *reinterpret_cast<uint32_t*>(a.codes + dst * (a.kpad >> 1) + 16 * kb + (lane >> 1)) = code;
+      if (lane == 1) *expert_sf_at(a, m, kb) = static_cast<uint8_t>(sb);
+    });
+  }
+}
+
+// Narrow rows (at most 16 blocks) without appended blocks, many of them: a group of 2^log_lanes lanes
+// for each, a block in each lane. A CTA for each is bound by the rate at which CTAs start (16384
+// rows of 256: 17.5 against 4.0 us; 131072 SwiGLU rows: 136 against 28 us). Rows of more than 16 blocks,
+// or with appended blocks, gain nothing from a warp for each (1056 channels: 28.7 against 23.8 us).
+template <int SRC>
+__global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts_narrow(QuantExpertsArgs a, int log_lanes) {
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, lanes = 1 << log_lanes, l = lane & (lanes - 1);
+  const int nblk = a.K >> 5;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kQexMaxWarps + (threadIdx.x >> 5);
+  const int64_t src = (warp << (5 - log_lanes)) + (lane >> log_lanes);
+  pdl_wait();
+  int64_t n = a.n;
+  if (SRC == kQexSwiglu) n = min(n, static_cast<int64_t>(a.p.offsets[a.experts]));
+  const bool valid = src < n;
+  const int nrows = SRC == kQexTokens ? a.k : 1;
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = 0u;
+  if (valid && l < nblk) load_block<SRC>(a.x + src * a.ldx, a.K, 32 * l, w);
+  uint32_t sb;
+  bool zero;
+  const uint4 cc = code_block(w, sb, zero);
+  const uint32_t joined = join_scales(sb);
+  for (int j0 = 0; j0 < nrows; j0 += lanes) {
+    int dsts = -1, sfrs = -1;  // lane j of the group: a destination
+    if (valid && j0 + l < nrows) expert_places<SRC>(a, src, j0 + l, dsts, sfrs);
+    const int nj = min(lanes, nrows - j0);
+    for (int j = 0; j < nj; ++j) {
+      const int64_t dst = __shfl_sync(0xFFFFFFFFu, dsts, j, lanes), m = __shfl_sync(0xFFFFFFFFu, sfrs, j, lanes);
+      if (dst >= 0) store_block(a, dst, m, l, nblk, cc, sb, joined);
     }
   }
 }

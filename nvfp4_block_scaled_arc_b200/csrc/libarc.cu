@@ -458,7 +458,8 @@ arc_status quantize_experts(const void* x, int64_t ldx, int64_t K, const int32_t
   if (K <= 0 || K % 32 || r < 0 || r % 32 || r > K || ldx < width || (r > 0 && !idx)) return ARC_ERR_INVALID_ARG;
   if (K > (1ll << 20) || r > 32767) return ARC_ERR_UNSUPPORTED;
   if (!al16(x) || (ldx * 2) % 16 || !al16(plan) || !al16(codes) || !al16(sf)) return ARC_ERR_ALIGNMENT;
-  st = device_check(nullptr);
+  int sms = 0;
+  st = device_check(&sms);
   if (st != ARC_OK) return st;
   arc::QuantExpertsArgs a;
   a.x = static_cast<const __nv_bfloat16*>(x);
@@ -475,12 +476,21 @@ arc_status quantize_experts(const void* x, int64_t ldx, int64_t K, const int32_t
   a.experts = experts;
   a.codes = codes;
   a.sf = sf;
+  const int nblk = static_cast<int>(K / 32);
+  int log_lanes = 5;  // of a group that holds the row, a block in each lane
+  while (log_lanes > 0 && (1 << (log_lanes - 1)) >= nblk) --log_lanes;
+  // narrow rows without appended blocks share warps once there are a few for each SM's warps
+  if (r == 0 && log_lanes < 5 && a.n >= 4ll * sms * arc::kQexMaxWarps) {
+    const int64_t per_block = static_cast<int64_t>(arc::kQexMaxWarps) << (5 - log_lanes);
+    return launch_pdl(arc::k_quant_experts_narrow<SRC>, (a.n + per_block - 1) / per_block, 32 * arc::kQexMaxWarps, 0, 1,
+                      S(stream), a, log_lanes);
+  }
   // as many warps as the row has segments of 1024 values, or as divide them into the fewest rounds
-  const int nseg = static_cast<int>((K / 32 + 31) / 32);
+  const int nseg = (nblk + 31) / 32;
   const int rounds = (nseg + arc::kQexMaxWarps - 1) / arc::kQexMaxWarps;
   const int warps = (nseg + rounds - 1) / rounds;
-  return launch_pdl(arc::k_quant_experts<SRC>, a.n, 32 * warps, r > 0 ? static_cast<size_t>(K / 32) : 0, 1, S(stream),
-                    a);
+  return launch_pdl(arc::k_quant_experts<SRC>, a.n, 32 * warps, r > 0 ? static_cast<size_t>(nblk) : 0, 1,
+                    S(stream), a);
 }
 
 template <int KIND, int MAXN>

@@ -229,7 +229,10 @@ def _coded_out(plan, k_aug):
 
 QUANTS = [(1, 8, 16, 64, 0, "skewed"), (1, 2, 4, 4096, 64, "skewed"), (37, 3, 5, 96, 32, "drop"),
           (130, 2, 8, 1056, 128, "repeat"), (300, 1, 3, 512, 512, "one"), (9, 40, 64, 288, 0, "skewed"),
-          (200, 4, 64, 2048, 96, "drop"), (5, 2, 3, 32, 32, "drop")]
+          (200, 4, 64, 2048, 96, "drop"), (5, 2, 3, 32, 32, "drop"),
+          # many narrow rows (lane groups of 8, 4, 1, 16 and 2)
+          (5003, 3, 8, 256, 0, "drop"), (4801, 1, 5, 96, 0, "skewed"), (4737, 5, 4, 32, 0, "repeat"),
+          (4750, 1, 2, 480, 0, "drop"), (4799, 2, 512, 64, 0, "skewed")]
 
 
 @pytest.mark.parametrize("tokens,k,experts,K,r,how", QUANTS)
