@@ -415,8 +415,10 @@ arc_status launch_pdl(void (*kern)(P...), int64_t grid, int block, size_t smem, 
 }
 
 // Shape of a move kernel's grid: U 16-byte vectors per lane, groups of 2^log_lanes lanes, nseg
-// segments of a row. Four vectors per lane where that still fills the machine (16384 tokens of 2 x
-// 4096: 68 against 86 us), one where a few tokens are spread over more warps.
+// segments of a row. Four vectors per lane where that still gives every SM a number of warps, one
+// where a few tokens are spread over more. For the combine 16 an SM (1024 tokens of 8 x 4096: 12.5
+// against 14.7 us; 16384 of 2 x 4096: 64.7 against 82.4 us), for the dispatch, which has k rows' stores in
+// flight for one load, 32 (17.0 against 13.4 us; 62.3 against 77.8 us).
 struct MoveShape {
   int u, log_lanes, nseg;
   int64_t blocks;
@@ -431,9 +433,9 @@ MoveShape move_shape(int64_t items, int64_t vecs, int u) {
   m.blocks = (groups + per_block - 1) / per_block;
   return m;
 }
-MoveShape move_shape(int64_t tokens, int64_t vecs) {
+MoveShape move_shape_fill(int64_t tokens, int64_t vecs, int sm_warps) {
   const MoveShape four = move_shape(tokens, vecs, 4);
-  return four.blocks * (arc::kMoveThreads / 32) >= 148 * 32 ? four : move_shape(tokens, vecs, 1);
+  return four.blocks * (arc::kMoveThreads / 32) >= 148 * sm_warps ? four : move_shape(tokens, vecs, 1);
 }
 
 arc_status move_check(int64_t d, int64_t ld_a, int64_t ld_b, const void* a, const void* b, const int32_t* plan,
@@ -827,7 +829,7 @@ arc_status arc_dispatch_experts_bf16(const void* x_bf16, int64_t ldx, int64_t d,
   arc_status st = move_check(d, ldx, ld_rows, x_bf16, rows_bf16, plan, tokens, k, experts);
   if (st != ARC_OK) return st;
   if ((st = device_check(nullptr)) != ARC_OK) return st;
-  const MoveShape m = move_shape(tokens, d / 8);
+  const MoveShape m = move_shape_fill(tokens, d / 8, 32);
   return launch_pdl(m.u == 4 ? arc::k_dispatch<4> : arc::k_dispatch<1>, m.blocks, arc::kMoveThreads, 0, 1, S(stream),
                     static_cast<const __nv_bfloat16*>(x_bf16), ldx, static_cast<int>(d / 8), m.log_lanes, m.nseg,
                     arc::plan_sections(plan, tokens * k, experts), tokens, k, static_cast<__nv_bfloat16*>(rows_bf16),
@@ -839,12 +841,13 @@ static arc_status combine_rows(const void* rows, int64_t ld_rows, int64_t d, con
                                int64_t ld_add, void* y, int64_t ldy, arc_stream_t stream) {
   arc_status st = device_check(nullptr);
   if (st != ARC_OK) return st;
-  const MoveShape m = move_shape(tokens, d / 8);
+  const MoveShape m = move_shape_fill(tokens, d / 8, 16);
   const auto kern = m.log_lanes == 5 ? (m.u == 4 ? arc::k_combine<4, true> : arc::k_combine<1, true>)
                                      : (m.u == 4 ? arc::k_combine<4, false> : arc::k_combine<1, false>);
   return launch_pdl(kern, m.blocks, arc::kMoveThreads, 0, 1, S(stream), static_cast<const __nv_bfloat16*>(rows),
-                    ld_rows, static_cast<int>(d / 8), m.log_lanes, m.nseg, weights, ld_weights, arc::plan_sections(plan, tokens * k, experts), tokens, k,
-                    static_cast<const __nv_bfloat16*>(add), ld_add, static_cast<__nv_bfloat16*>(y), ldy);
+                    ld_rows, static_cast<int>(d / 8), m.log_lanes, m.nseg, weights, ld_weights,
+                    arc::plan_sections(plan, tokens * k, experts), tokens, k, static_cast<const __nv_bfloat16*>(add),
+                    ld_add, static_cast<__nv_bfloat16*>(y), ldy);
 }
 
 arc_status arc_dispatch_experts_grad_bf16(const void* d_rows_bf16, int64_t ld_rows, int64_t d, const int32_t* plan,
@@ -883,8 +886,9 @@ arc_status arc_combine_experts_grad_bf16(const void* d_y_bf16, int64_t ld_dy, co
   const MoveShape m = move_shape(slots, std::min<int64_t>(d / 8, 128), 4);  // one group per slot
   return launch_pdl(arc::k_combine_grad, m.blocks, arc::kMoveThreads, 0, 1, S(stream),
                     static_cast<const __nv_bfloat16*>(d_y_bf16), ld_dy, static_cast<const __nv_bfloat16*>(rows_bf16),
-                    ld_rows, static_cast<int>(d / 8), m.log_lanes, weights, ld_weights, arc::plan_sections(plan, slots, experts), tokens, k,
-                    static_cast<__nv_bfloat16*>(d_rows_bf16), ld_drows, d_weights, ld_dw);
+                    ld_rows, static_cast<int>(d / 8), m.log_lanes, weights, ld_weights,
+                    arc::plan_sections(plan, slots, experts), tokens, k, static_cast<__nv_bfloat16*>(d_rows_bf16),
+                    ld_drows, d_weights, ld_dw);
 }
 
 arc_status arc_quantize_act_experts_mxfp4(const void* x_bf16, int64_t ldx, int64_t K, const int32_t* d_idx, int32_t r,
