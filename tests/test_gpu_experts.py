@@ -158,7 +158,9 @@ def test_combine_gradients(tokens, k, experts, d, how, pad):
     assert (np.abs(f64(d_rows)[:used] - ref) <= (BF16_HALF_STEP + 2 * F32_HALF_STEP) * np.abs(ref)).all()
     assert torch.isnan(d_rows[used:]).all() and (d_w[:, k] == -7.0).all()
     prod = np.repeat(f64(dy), k, axis=0) * _by_slot(f64(rows), p)
-    tol = (d / 32 + 8) * F32_HALF_STEP * np.abs(prod).sum(1)
+    # a lane adds up at most three rounds of four vectors of 8 values, or d / 32 of them and a vector's
+    # rest where 32 lanes share the row; five shuffles join the lanes
+    tol = (max(d / 32 + 8, 96) + 5) * F32_HALF_STEP * np.abs(prod).sum(1)
     assert (np.abs(f64(d_w[:, :k]).reshape(-1) - prod.sum(1)) <= tol).all()
     # the rows' gradient in the rows' own place
     want = d_rows.clone()
