@@ -66,11 +66,12 @@ __host__ __device__ constexpr int row_box_height(int index) { return index == 0 
 
 constexpr int kExpertBarBytes = 384;
 
-// Shared memory behind the stages: staging, barriers, first tile and first row of every expert.
+// Shared memory behind the stages: staging, barriers, and every expert's first tile, first row and first
+// block of scale bytes.
 template <int KIND, int MAXN>
 constexpr int expert_gemm_smem_bytes(int experts) {
   return ExpertGemmTraits<KIND, MAXN>::STAGES * ExpertGemmTraits<KIND, MAXN>::STAGE_BYTES + 8 * kExpertEpiBytes +
-         kExpertBarBytes + 2 * (experts + 1) * 4 + 1024;
+         kExpertBarBytes + 3 * (experts + 1) * 4 + 1024;
 }
 
 struct ExpertGemmArgs {
@@ -240,7 +241,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* first = reinterpret_cast<int*>(staging + 8 * kExpertEpiBytes + kExpertBarBytes);  // [E + 1]
-  int* offsets = first + g.experts + 1;                                      // [E + 1]
+  int* offsets = first + g.experts + 1;                                                          // [E + 1]
+  int* blocks = offsets + g.experts + 1;                                                         // [E + 1]
   static_assert((3 * T::STAGES + 2 * T::ACC_STAGES + 1) * 8 + 8 <= kExpertBarBytes, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -263,17 +265,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tma_prefetch_desc(&tmY);
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the other CTA's barriers are initialised
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   pdl_wait();  // the plan and the operands come from earlier kernels
   // A buffer that no plan was written to is reported and has no tiles.
   bool bad = false;
   for (int e = threadIdx.x; e <= g.experts; e += kGemmThreads) {
-    const int at = g.p.offsets[e], next = g.p.offsets[min(e + 1, g.experts)];
+    const int at = g.p.offsets[e], next = g.p.offsets[min(e + 1, g.experts)], blk = MX4 ? g.p.blocks[e] : 0;
     offsets[e] = at;
+    blocks[e] = blk;
     bad |= at < 0 || next < at || next > g.slots;
-    if (MX4 && e < g.experts && !bad) {
-      const int blk = g.p.blocks[e];
-      bad |= blk < 0 || 128ll * (blk + static_cast<int64_t>((next - at + 127) / 128)) > g.sfx_rows;
-    }
+    if (MX4 && !bad) bad = blk < 0 || 128ll * (blk + static_cast<int64_t>((next - at + 127) / 128)) > g.sfx_rows;
   }
   bad = __syncthreads_or(bad);
   if (bad && threadIdx.x == 0) set_status(kStatusInvalidArg);
@@ -293,11 +298,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       run += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
   }
-  tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // the other CTA's barriers are initialised
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   const int ntiles = bad ? 0 : first[g.experts] * g.tiles_w;
   auto tile = [&](int t) { return expert_tile(t, first, offsets, g.experts, g.tiles_w, g.group_m); };
 
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int box_x = static_cast<int>(min(static_cast<int64_t>(row_box_height(bi)), g.slots));
       const CUtensorMap* map_x = &tmX.box[bi];
       const bool has_sfw = MX4 && 2 * at.tw + static_cast<int>(rank) < g.nblk128;
-      const uint8_t* sfx = MX4 ? g.sfx + (128ll * g.p.blocks[at.e] + at.row) * 8 : nullptr;
+      const uint8_t* sfx = MX4 ? g.sfx + (128ll * blocks[at.e] + at.row) * 8 : nullptr;
       const uint32_t bytes0 =
           static_cast<uint32_t>(g.box_w + box_x) * 128u + (MX4 ? static_cast<uint32_t>(at.n) * 8u : 0u);
       for (int ks = 0; ks < g.kstages; ++ks) {
