@@ -671,6 +671,14 @@ def _on(fn: str, dev: int, stream):
     return torch.cuda.stream(stream)
 
 
+def _new_plan(ids: torch.Tensor, tokens: int, k: int, experts: int) -> ExpertPlan:
+    """An ExpertPlan around a new buffer, without the checks of one that a caller brings."""
+    p, slots = ExpertPlan.__new__(ExpertPlan), tokens * k
+    p.buf = ids.new_empty(2 * ((experts + 64) // 64 * 64) + 3 * ((slots + 63) // 64 * 64), dtype=_I32)
+    p.tokens, p.k, p.experts, p.slots = tokens, k, experts, slots
+    return p
+
+
 def expert_plan(ids: torch.Tensor, experts: int, out: ExpertPlan | None = None, stream=None) -> ExpertPlan:
     """arc_expert_plan: the slots of expert ids [T, k] (int32 or int64) sorted by expert; ids outside
     [0, experts) give their slots no row."""
@@ -684,8 +692,7 @@ def expert_plan(ids: torch.Tensor, experts: int, out: ExpertPlan | None = None, 
             return expert_plan(ids, experts, out)
     ld = _rows_of(fn, "ids", ids, dtype, dev, shape)
     if out is None:
-        n = 2 * _pad64(experts + 1) + 3 * _pad64(T * k)
-        out = ExpertPlan(ids.new_empty(n, dtype=_I32), T, k, experts)
+        out = _new_plan(ids, T, k, experts)
     elif (out.tokens, out.k, out.experts) != (T, k, experts):
         raise ValueError("expert_plan: out was made for other sizes")
     _check("arc_expert_plan", lib().arc_expert_plan(
@@ -702,7 +709,7 @@ def dispatch_experts(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None
             return dispatch_experts(x, plan, out)
     ld = _rows_of(fn, "x", x, _BF16, dev, (T, d))
     if out is None:
-        out, ld_out = x.new_empty((T * k, d)), d
+        out, ld_out = x.new_empty(T * k, d), d
     else:
         ld_out = _rows_of(fn, "out", out, _BF16, dev, (T * k, d))
     _check("arc_dispatch_experts_bf16", lib().arc_dispatch_experts_bf16(
@@ -719,7 +726,7 @@ def dispatch_experts_grad(d_rows: torch.Tensor, plan: ExpertPlan, out: torch.Ten
             return dispatch_experts_grad(d_rows, plan, out)
     ld = _rows_of(fn, "d_rows", d_rows, _BF16, dev, (T * k, d))
     if out is None:
-        out, ld_out = d_rows.new_empty((T, d)), d
+        out, ld_out = d_rows.new_empty(T, d), d
     else:
         ld_out = _rows_of(fn, "out", out, _BF16, dev, (T, d))
     _check("arc_dispatch_experts_grad_bf16", lib().arc_dispatch_experts_grad_bf16(
@@ -739,7 +746,7 @@ def combine_experts(rows: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
     ld = _rows_of(fn, "rows", rows, _BF16, dev, (T * k, d))
     ld_w = _rows_of(fn, "weights", weights, _F32, dev, (T, k))
     if out is None:
-        out, ld_out = rows.new_empty((T, d)), d
+        out, ld_out = rows.new_empty(T, d), d
     else:
         ld_out = _rows_of(fn, "out", out, _BF16, dev, (T, d))
     _check("arc_combine_experts_bf16", lib().arc_combine_experts_bf16(
@@ -762,9 +769,9 @@ def combine_experts_grad(d_y: torch.Tensor, rows: torch.Tensor, weights: torch.T
     ld = _rows_of(fn, "rows", rows, _BF16, dev, (T * k, d))
     ld_w = _rows_of(fn, "weights", weights, _F32, dev, (T, k))
     if d_rows is None:
-        d_rows = rows.new_empty((T * k, d))
+        d_rows = rows.new_empty(T * k, d)
     if d_weights is None:
-        d_weights = weights.new_empty((T, k))
+        d_weights = weights.new_empty(T, k)
     _check("arc_combine_experts_grad_bf16", lib().arc_combine_experts_grad_bf16(
         d_y.data_ptr(), ld_dy, rows.data_ptr(), ld, d, weights.data_ptr(), ld_w, _plan_ptr(fn, plan, dev), T, k,
         plan.experts, d_rows.data_ptr(), _rows_of(fn, "d_rows", d_rows, _BF16, dev, (T * k, d)),
@@ -871,7 +878,7 @@ def gemm_experts_mxfp4(a: ExpertMXFP4, w: ExpertWeightMXFP4, plan: ExpertPlan, o
     _flat(fn, "w.codes", w.codes, _U8, dev, w.experts * n * kp // 2)
     _flat(fn, "w.sf", w.sf, _U8, dev, w.experts * ((n + 127) // 128) * ((kp + 127) // 128) * 512)
     if out is None:
-        out, ld_out = a.buf.new_empty((S, n), dtype=_BF16), n
+        out, ld_out = a.buf.new_empty(S, n, dtype=_BF16), n
     else:
         ld_out = _rows_of(fn, "out", out, _BF16, dev, (S, n))
     codes = a.buf.data_ptr()
@@ -894,7 +901,7 @@ def gemm_experts_bf16(rows: torch.Tensor, w: torch.Tensor, plan: ExpertPlan, out
     ld = _rows_of(fn, "rows", rows, _BF16, dev, (S, K))
     ld_w = _expert_weight_ld(fn, w, dev, plan.experts, N, K)
     if out is None:
-        out, ld_out = rows.new_empty((S, N)), N
+        out, ld_out = rows.new_empty(S, N), N
     else:
         ld_out = _rows_of(fn, "out", out, _BF16, dev, (S, N))
     _check("arc_gemm_experts_bf16", lib().arc_gemm_experts_bf16(
