@@ -562,15 +562,15 @@ __device__ __forceinline__ uint4 code_block(const uint32_t (&w)[16], uint32_t& s
   return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
-// E2M1 code of one value (round to nearest even, saturating at +-6).
-__device__ __forceinline__ uint32_t e2m1_rn_sat(float v) {
+// E2M1 codes of two values (round to nearest even, saturating at +-6), the first's lowest.
+__device__ __forceinline__ uint32_t e2m1x2_rn_sat(float lo, float hi) {
   uint32_t out;
   asm("{\n\t.reg .b8 b;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
       "cvt.u32.u8 %0, b;\n\t}"
       : "=r"(out)
-      : "f"(v), "f"(0.0f));
-  return out & 15u;
+      : "f"(lo), "f"(hi));
+  return out;
 }
 
 // Residual of an outlier channel with value bits xw in a block of scale byte t, the code formed
@@ -578,7 +578,7 @@ __device__ __forceinline__ uint32_t e2m1_rn_sat(float v) {
 __device__ __forceinline__ float outlier_residual(uint32_t xw, uint32_t t) {
   const float xv = __uint_as_float(xw << 16);
   if (t == kMxZeroBlock) return xv;
-  return __fsub_rn(xv, __fmul_rn(e2m1_value(e2m1_rn_sat(__fmul_rn(xv, mx_inv_scale(t)))), mx_scale(t)));
+  return __fsub_rn(xv, __fmul_rn(e2m1_value(e2m1x2_rn_sat(__fmul_rn(xv, mx_inv_scale(t)), 0.0f) & 15u), mx_scale(t)));
 }
 
 // The appended block of the warp's 32 residuals: its scale byte, and eight lanes' codes as one 32-bit
@@ -586,10 +586,22 @@ __device__ __forceinline__ float outlier_residual(uint32_t xw, uint32_t t) {
 __device__ __forceinline__ uint32_t code_residuals(float res, uint32_t& sb) {
   const uint32_t am = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(res)));
   sb = mx_scale_byte(am);
-  uint32_t code = am == 0u ? 0u : e2m1_rn_sat(__fmul_rn(res, mx_inv_scale(sb)));
+  uint32_t code = am == 0u ? 0u : e2m1x2_rn_sat(__fmul_rn(res, mx_inv_scale(sb)), 0.0f) & 15u;
   code |= __shfl_down_sync(0xFFFFFFFFu, code, 1) << 4;
   code |= __shfl_down_sync(0xFFFFFFFFu, code, 2) << 8;
   return code | __shfl_down_sync(0xFFFFFFFFu, code, 4) << 16;
+}
+
+// The same for a half warp's 32 residuals, two in each lane: the word in every fourth lane.
+__device__ __forceinline__ uint32_t code_residuals(float r0, float r1, uint32_t& sb) {
+  uint32_t am = max(__float_as_uint(fabsf(r0)), __float_as_uint(fabsf(r1)));
+#pragma unroll
+  for (int o = 8; o; o >>= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+  sb = mx_scale_byte(am);
+  const float inv = mx_inv_scale(sb);
+  uint32_t code = am == 0u ? 0u : e2m1x2_rn_sat(__fmul_rn(r0, inv), __fmul_rn(r1, inv));
+  code |= __shfl_down_sync(0xFFFFFFFFu, code, 1) << 8;
+  return code | __shfl_down_sync(0xFFFFFFFFu, code, 2) << 16;
 }
 
 // Scale byte kb of place m: 8 bytes (a K = 256 pipeline stage of the product) per row and stage.
@@ -698,15 +710,18 @@ __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts(QuantExpert
   }
 }
 
-// Narrow rows (at most 16 blocks) without appended blocks, many of them: a group of 2^log_lanes lanes
-// for each, a block in each lane. A CTA for each is bound by the rate at which CTAs start (16384
-// rows of 256: 17.5 against 4.0 us; 131072 SwiGLU rows: 136 against 28 us). Rows of more than 16 blocks,
-// or with appended blocks, gain nothing from a warp for each (1056 channels: 28.7 against 23.8 us).
+// Many rows of at most 32 blocks: a group of 2^log_lanes lanes for each (16 or 32 where there are appended
+// blocks), a block in each lane. With a CTA for each row most lanes of narrow rows idle, and the rows
+// are bound by instructions (16384 rows of 256: 17.5 against 3.7 us, of 512 with r 64: 17.8 against 10.0 us;
+// 131072 SwiGLU rows: 136 against 30 us and 140 against 78 us).
+// A half warp takes an appended block, a lane two of its channels; the primary blocks' scale bytes come
+// by shuffle. Where a row fills several warps that form is no faster (4096 channels, r 256: 53.5 against
+// 55.2 us), nor are several rows a CTA (27.8 against 23.6 us, SwiGLU, 1056 channels).
 template <int SRC>
 __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts_narrow(QuantExpertsArgs a, int log_lanes) {
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, lanes = 1 << log_lanes, l = lane & (lanes - 1);
-  const int nblk = a.K >> 5;
+  const int lane = threadIdx.x & 31, lanes = 1 << log_lanes, l = lane & (lanes - 1), hl = lane & 15;
+  const int nblk = a.K >> 5, nres = a.r >> 5;
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * kQexMaxWarps + (threadIdx.x >> 5);
   const int64_t src = (warp << (5 - log_lanes)) + (lane >> log_lanes);
   pdl_wait();
@@ -714,22 +729,69 @@ __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts_narrow(Quan
   if (SRC == kQexSwiglu) n = min(n, static_cast<int64_t>(a.p.offsets[a.experts]));
   const bool valid = src < n;
   const int nrows = SRC == kQexTokens ? a.k : 1;
+  const __nv_bfloat16* row = a.x + src * a.ldx;
+  int dst0 = -1, sfr0 = -1;  // lane j of the group: the j-th destination (a group's lanes at a time)
+  if (valid && l < nrows) expert_places<SRC>(a, src, l, dst0, sfr0);
+  int c0 = -1, c1 = -1;  // the values of an appended block, two a lane
+  uint32_t og = 0, ou = 0;
+  auto outlier = [&](int at, int shift) {
+    const int c = a.idx[at];
+    if (static_cast<unsigned>(c) >= static_cast<unsigned>(a.K)) {
+      if (src == 0) set_status(kStatusInvalidArg);
+      return -1;
+    }
+    og |= ld_u16(row + c) << shift;
+    if constexpr (SRC == kQexSwiglu) ou |= ld_u16(row + a.K + c) << shift;
+    return c;
+  };
+  auto outliers = [&](int rb) {
+    c0 = c1 = -1;
+    og = ou = 0;
+    if (valid && rb < nres) {
+      c0 = outlier(32 * rb + 2 * hl, 0);
+      c1 = outlier(32 * rb + 2 * hl + 1, 16);
+    }
+  };
+  if (nres > 0) outliers(l >> 4);
   uint32_t w[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) w[i] = 0u;
-  if (valid && l < nblk) load_block<SRC>(a.x + src * a.ldx, a.K, 32 * l, w);
+  if (valid && l < nblk) load_block<SRC>(row, a.K, 32 * l, w);
   uint32_t sb;
   bool zero;
   const uint4 cc = code_block(w, sb, zero);
   const uint32_t joined = join_scales(sb);
-  for (int j0 = 0; j0 < nrows; j0 += lanes) {
-    int dsts = -1, sfrs = -1;  // lane j of the group: a destination
-    if (valid && j0 + l < nrows) expert_places<SRC>(a, src, j0 + l, dsts, sfrs);
-    const int nj = min(lanes, nrows - j0);
-    for (int j = 0; j < nj; ++j) {
-      const int64_t dst = __shfl_sync(0xFFFFFFFFu, dsts, j, lanes), m = __shfl_sync(0xFFFFFFFFu, sfrs, j, lanes);
-      if (dst >= 0) store_block(a, dst, m, l, nblk, cc, sb, joined);
+  auto each_place = [&](auto&& store) {
+    for (int j0 = 0; j0 < nrows; j0 += lanes) {
+      int dsts = dst0, sfrs = sfr0;
+      if (j0) {
+        dsts = -1;
+        if (valid && j0 + l < nrows) expert_places<SRC>(a, src, j0 + l, dsts, sfrs);
+      }
+      const int nj = min(lanes, nrows - j0);
+      for (int j = 0; j < nj; ++j) {
+        const int64_t dst = __shfl_sync(0xFFFFFFFFu, dsts, j, lanes), m = __shfl_sync(0xFFFFFFFFu, sfrs, j, lanes);
+        if (dst >= 0) store(dst, m);
+      }
     }
+  };
+  each_place([&](int64_t dst, int64_t m) { store_block(a, dst, m, l, nblk, cc, sb, joined); });
+  if (zero) sb = kMxZeroBlock;
+  for (int rb0 = 0; rb0 < nres; rb0 += lanes >> 4) {  // a half warp a block
+    const int rb = rb0 + (l >> 4), kb = nblk + rb;
+    if (rb0) outliers(rb);
+    const uint32_t t0 = __shfl_sync(0xFFFFFFFFu, sb, max(c0, 0) >> 5, lanes);
+    const uint32_t t1 = __shfl_sync(0xFFFFFFFFu, sb, max(c1, 0) >> 5, lanes);
+    const uint32_t xw = SRC == kQexSwiglu ? silu_mul_pair(og, ou) : og;
+    const float r0 = c0 >= 0 ? outlier_residual(xw & 0xFFFFu, t0) : 0.0f;
+    const float r1 = c1 >= 0 ? outlier_residual(xw >> 16, t1) : 0.0f;
+    uint32_t sbr;
+    const uint32_t code = code_residuals(r0, r1, sbr);
+    each_place([&](int64_t dst, int64_t m) {
+      if (rb >= nres) return;
+      if ((hl & 3) == 0) *reinterpret_cast<uint32_t*>(a.codes + dst * (a.kpad >> 1) + 16 * kb + hl) = code;
+      if (hl == 1) *expert_sf_at(a, m, kb) = static_cast<uint8_t>(sbr);
+    });
   }
 }
 

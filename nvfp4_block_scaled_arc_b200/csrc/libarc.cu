@@ -479,10 +479,10 @@ arc_status quantize_experts(const void* x, int64_t ldx, int64_t K, const int32_t
   a.codes = codes;
   a.sf = sf;
   const int nblk = static_cast<int>(K / 32);
-  int log_lanes = 5;  // of a group that holds the row, a block in each lane
-  while (log_lanes > 0 && (1 << (log_lanes - 1)) >= nblk) --log_lanes;
-  // narrow rows without appended blocks share warps once there are a few for each SM's warps
-  if (r == 0 && log_lanes < 5 && a.n >= 4ll * sms * arc::kQexMaxWarps) {
+  // Rows of at most 32 blocks are dealt to lane groups once there are a few for each SM's warps.
+  if (nblk <= 32 && a.n >= 4ll * sms * arc::kQexMaxWarps) {
+    int log_lanes = 5;  // of a group that holds the row, a block in each lane
+    while (log_lanes > (r > 0 ? 4 : 0) && (1 << (log_lanes - 1)) >= nblk) --log_lanes;
     const int64_t per_block = static_cast<int64_t>(arc::kQexMaxWarps) << (5 - log_lanes);
     return launch_pdl(arc::k_quant_experts_narrow<SRC>, (a.n + per_block - 1) / per_block, 32 * arc::kQexMaxWarps, 0, 1,
                       S(stream), a, log_lanes);

@@ -234,7 +234,10 @@ QUANTS = [(1, 8, 16, 64, 0, "skewed"), (1, 2, 4, 4096, 64, "skewed"), (37, 3, 5,
           (200, 4, 64, 2048, 96, "drop"), (5, 2, 3, 32, 32, "drop"),
           # many narrow rows (lane groups of 8, 4, 1, 16 and 2)
           (5003, 3, 8, 256, 0, "drop"), (4801, 1, 5, 96, 0, "skewed"), (4737, 5, 4, 32, 0, "repeat"),
-          (4750, 1, 2, 480, 0, "drop"), (4799, 2, 512, 64, 0, "skewed")]
+          (4750, 1, 2, 480, 0, "drop"), (4799, 2, 512, 64, 0, "skewed"),
+          # with appended blocks, and of a whole warp
+          (4751, 2, 8, 512, 96, "drop"), (4803, 1, 4, 64, 64, "skewed"), (4740, 3, 5, 736, 160, "repeat"),
+          (4738, 40, 64, 32, 32, "skewed"), (4757, 1, 3, 1024, 0, "drop")]
 
 
 @pytest.mark.parametrize("tokens,k,experts,K,r,how", QUANTS)
