@@ -173,8 +173,11 @@ __device__ __forceinline__ void expert_mma(uint32_t d_tmem, uint64_t dw, uint64_
 __device__ __forceinline__ void lds_u32x2(uint32_t addr, uint32_t& a, uint32_t& b) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
 }
-__device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(v)) : "memory");
+// Four 8 x 8 matrices of 16-bit values, transposed: lane 8 i + r gives the address of matrix i's column r.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -186,13 +189,12 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 
-// 32 lanes x 16 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// 16 lanes x 16 consecutive 32-bit columns: lane t of the warp gets, in r[4 c + 2 h] and the next, columns
+// 8 c + 2 (t % 4) and the next of TMEM lane t / 4 + 8 h.
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 
 // Where tile t lies: expert, feature tile, first row within the expert, rows of the expert from
@@ -503,6 +505,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int q = warp & 3, half = (warp - kGemmEpiWarp0) >> 2;
     uint8_t* stg = staging + (warp - kGemmEpiWarp0) * kExpertEpiBytes;
     const uint32_t stg32 = smem_u32(stg);
+    // A staged row is 64 bytes, its 16-byte parts permuted by the map's 64-byte swizzle (part ^ (row / 2) % 4),
+    // which keeps the eight rows of a matrix on different banks.
+    const uint32_t st_addr = stg32 + (lane & 7) * 64 + 16 * ((lane >> 3) ^ ((lane >> 1) & 3));
     uint32_t acc = 0, acc_phase = 0;
     for (int t = unit; t < ntiles; t += units) {
       const ExpertTile at = tile(t);
@@ -517,15 +522,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
       for (int c = 0; c < NC; c += 2) {
         if (32 * c + 16 * half < at.n) {
-          uint32_t r0[16], r1[16];
-          tmem_ld_32x32b_x16(tbase + 32 * c, r0);
-          tmem_ld_32x32b_x16(tbase + 32 * c + 32, r1);
+          uint32_t r[2][2][8];  // chunk, lane half
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            tmem_ld_16x256b_x2(tbase + 32 * (c + (i >> 1)) + (static_cast<uint32_t>(16 * (i & 1)) << 16),
+                               r[i >> 1][i & 1]);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            pk[8 * c + j] = pack_bf16x2_rn(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]));
-            pk[8 * c + 8 + j] = pack_bf16x2_rn(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]));
-          }
+          for (int i = 0; i < 16; ++i)  // pk[8 c + 4 b + m]: rows 8 b .. of the chunk, features 8 m ..
+            pk[8 * c + i] = pack_bf16x2_rn(__uint_as_float(r[i >> 3][(i >> 1) & 1][4 * ((i >> 2) & 1) + 2 * (i & 1)]),
+                                           __uint_as_float(r[i >> 3][(i >> 1) & 1][4 * ((i >> 2) & 1) + 2 * (i & 1) + 1]));
         }
       }
       tc_fence_before();
@@ -536,11 +542,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int r0 = 32 * c + 16 * half;  // first row of the chunk within the tile
         const int nrows = at.left - r0;
         if (r0 < at.n && nrows > 0 && f0 < g.N) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            sts_u16(stg32 + (2 * j) * 64 + lane * 2, pk[8 * c + j]);
-            sts_u16(stg32 + (2 * j + 1) * 64 + lane * 2, pk[8 * c + j] >> 16);
-          }
+          stmatrix_x4_trans(st_addr, pk[8 * c], pk[8 * c + 1], pk[8 * c + 2], pk[8 * c + 3]);
+          stmatrix_x4_trans(st_addr + 8 * 64, pk[8 * c + 4], pk[8 * c + 5], pk[8 * c + 6], pk[8 * c + 7]);
           if (nrows >= 16) {
             fence_proxy_async_smem();
             __syncwarp();
@@ -556,7 +559,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int rr = lane >> 1, f = 16 * (lane & 1);
             if (rr < nrows) {
               __nv_bfloat16* dst = g.y + (y0 + r0 + rr) * g.ldy + f0 + f;
-              const uint4 a = lds_u32x4(stg32 + rr * 64 + 2 * f), b = lds_u32x4(stg32 + rr * 64 + 2 * f + 16);
+              const uint32_t at16 = static_cast<uint32_t>(2 * (lane & 1)) ^ ((rr >> 1) & 3);
+              const uint4 a = lds_u32x4(stg32 + rr * 64 + 16 * at16), b = lds_u32x4(stg32 + rr * 64 + 16 * (at16 ^ 1));
               if (f0 + f < g.N) *reinterpret_cast<uint4*>(dst) = a;
               if (f0 + f + 8 < g.N) *reinterpret_cast<uint4*>(dst + 8) = b;
             }

@@ -131,10 +131,11 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Y [outer, inner] bf16, row pitch in bytes, as the target of TMA stores (no swizzle; the staging
-// chunk is box_outer rows of box_inner values).
+// Y [outer, inner] bf16, row pitch in bytes, as the target of TMA stores (the staging chunk is
+// box_outer rows of box_inner values).
 bool make_store_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_bytes,
-                    uint32_t box_inner = 16, uint32_t box_outer = 32) {
+                    uint32_t box_inner = 16, uint32_t box_outer = 32,
+                    CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {inner, outer};
@@ -142,7 +143,7 @@ bool make_store_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t o
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -537,7 +538,7 @@ arc_status expert_gemm_launch(const void* a, int64_t a_pitch, const uint8_t* a_s
   arc::ExpertRowMaps tx;
   if (!make_map(&tw, dt, b, inner, static_cast<uint64_t>(experts * N), static_cast<uint64_t>(b_pitch), box, g.box_w) ||
       !make_store_map(&ty, y, static_cast<uint64_t>(N), static_cast<uint64_t>(slots), static_cast<uint64_t>(ldy) * 2,
-                      32, 16))
+                      32, 16, CU_TENSOR_MAP_SWIZZLE_64B))
     return ARC_ERR_CUDA;
   std::memset(&tx, 0, sizeof(tx));
   for (int i = 0; i <= arc::row_box_index(T::TN / 2); ++i)
