@@ -28,8 +28,9 @@
 // stage; the two K = 64 steps of a scale atom share the 32-bit cells and select their half by the
 // instruction's scale-factor id: the rows' cells at 8 (step / 2) + row / 32 (lane row % 32, in every
 // quarter), the weights' at 16 + 4 (step / 2) + quarter. BF16: two accumulators.
-// Epilogue: a lane is an output feature, a column a row of Y; 16 rows x 32 features are turned
-// in shared memory and stored by TMA.
+// Epilogue: a TMEM lane is an output feature, a column a row of Y; 16 rows x 32 features are turned on their
+// way into shared memory (stmatrix; with 16-bit stores from whole lanes 32768 rows of 512 -> 4096 took 93 us
+// instead of 85) and stored by TMA.
 // Every wait is bounded, as in k_gemm.
 #pragma once
 
@@ -49,6 +50,10 @@ struct ExpertGemmTraits {
   static constexpr int SFW_BYTES = MX4 ? 2 * 512 : 0, SFX_BYTES = MX4 ? TN * 8 : 0;
   static constexpr int STAGE_BYTES = (W_BYTES + X_BYTES + SFW_BYTES + SFX_BYTES + 1023) / 1024 * 1024;
   static constexpr int STAGES = TN == 256 ? 6 : MX4 ? 9 : 10;
+  // Staging chunks of an epilogue warp, as many as fit: a chunk's store is awaited before its next use. Short
+  // products are bound by their epilogue (32768 rows, 512 -> 4096: BF16 120 us with one chunk, 116 with three;
+  // MXFP4 80 us, and 75 with four chunks and five stages, which costs long products 2 %).
+  static constexpr int EPI_BUFS = TN == 256 ? (MX4 ? 1 : 3) : 2;
   static constexpr int ACC_STAGES = TN == 256 ? (MX4 ? 1 : 2) : 3;
   static constexpr int SF_COL0 = ACC_STAGES * TN, SF_SET_COLS = 32;
   static constexpr uint32_t IDESC0 = MX4 ? idesc_mxf4(TM, 0) : idesc_bf16(TM, 0);  // N is the tile's
@@ -70,7 +75,8 @@ constexpr int kExpertBarBytes = 384;
 // block of scale bytes.
 template <int KIND, int MAXN>
 constexpr int expert_gemm_smem_bytes(int experts) {
-  return ExpertGemmTraits<KIND, MAXN>::STAGES * ExpertGemmTraits<KIND, MAXN>::STAGE_BYTES + 8 * kExpertEpiBytes +
+  return ExpertGemmTraits<KIND, MAXN>::STAGES * ExpertGemmTraits<KIND, MAXN>::STAGE_BYTES +
+         8 * ExpertGemmTraits<KIND, MAXN>::EPI_BUFS * kExpertEpiBytes +
          kExpertBarBytes + 3 * (experts + 1) * 4 + 1024;
 }
 
@@ -146,6 +152,11 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
           smem_u32(bar)),
       "h"(static_cast<uint16_t>(3))
       : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {  // until at most N groups' sources are still read
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 template <class T>
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + T::STAGES * T::STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + 8 * kExpertEpiBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + 8 * T::EPI_BUFS * kExpertEpiBytes);
   uint64_t* empty = full + T::STAGES;
   uint64_t* ready = empty + T::STAGES;
   uint64_t* acc_full = ready + T::STAGES;
@@ -242,7 +253,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint64_t* drain = acc_empty + T::ACC_STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* first = reinterpret_cast<int*>(staging + 8 * kExpertEpiBytes + kExpertBarBytes);  // [E + 1]
+  int* first = reinterpret_cast<int*>(staging + 8 * T::EPI_BUFS * kExpertEpiBytes + kExpertBarBytes);  // [E + 1]
   int* offsets = first + g.experts + 1;                                                          // [E + 1]
   int* blocks = offsets + g.experts + 1;                                                         // [E + 1]
   static_assert((3 * T::STAGES + 2 * T::ACC_STAGES + 1) * 8 + 8 <= kExpertBarBytes, "barriers");
@@ -503,12 +514,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // 8 warps: warp w reads TMEM lane quarter w % 4 (32 features) and every other 16 columns (rows
     // of Y); all of them leave TMEM, rounded, before the first is stored.
     const int q = warp & 3, half = (warp - kGemmEpiWarp0) >> 2;
-    uint8_t* stg = staging + (warp - kGemmEpiWarp0) * kExpertEpiBytes;
-    const uint32_t stg32 = smem_u32(stg);
+    uint8_t* stg0 = staging + (warp - kGemmEpiWarp0) * (T::EPI_BUFS * kExpertEpiBytes);
     // A staged row is 64 bytes, its 16-byte parts permuted by the map's 64-byte swizzle (part ^ (row / 2) % 4),
     // which keeps the eight rows of a matrix on different banks.
-    const uint32_t st_addr = stg32 + (lane & 7) * 64 + 16 * ((lane >> 3) ^ ((lane >> 1) & 3));
+    const uint32_t st_at = (lane & 7) * 64 + 16 * ((lane >> 3) ^ ((lane >> 1) & 3));
     uint32_t acc = 0, acc_phase = 0;
+    int buf = 0;
     for (int t = unit; t < ntiles; t += units) {
       const ExpertTile at = tile(t);
       const int f0 = at.tw * T::TM + static_cast<int>(rank) * T::BM + q * 32;
@@ -542,6 +553,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int r0 = 32 * c + 16 * half;  // first row of the chunk within the tile
         const int nrows = at.left - r0;
         if (r0 < at.n && nrows > 0 && f0 < g.N) {
+          uint8_t* stg = stg0 + buf * kExpertEpiBytes;
+          buf = buf + 1 == T::EPI_BUFS ? 0 : buf + 1;
+          const uint32_t stg32 = smem_u32(stg), st_addr = stg32 + st_at;
+          if (lane == 0) bulk_wait_read<T::EPI_BUFS - 1>();  // the store that read this chunk last
+          __syncwarp();
           stmatrix_x4_trans(st_addr, pk[8 * c], pk[8 * c + 1], pk[8 * c + 2], pk[8 * c + 3]);
           stmatrix_x4_trans(st_addr + 8 * 64, pk[8 * c + 4], pk[8 * c + 5], pk[8 * c + 6], pk[8 * c + 7]);
           if (nrows >= 16) {
@@ -550,9 +566,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (lane == 0) {
               tma_store_2d(&tmY, stg, f0, static_cast<int32_t>(y0) + r0);  // clipped at the last feature
               bulk_commit_group();
-              bulk_wait_read_all();
             }
-            __syncwarp();
           } else {
             // the group ends inside these rows: only its own are stored, 16 features a lane
             __syncwarp();
@@ -564,6 +578,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               if (f0 + f < g.N) *reinterpret_cast<uint4*>(dst) = a;
               if (f0 + f + 8 < g.N) *reinterpret_cast<uint4*>(dst + 8) = b;
             }
+            if (lane == 0) bulk_commit_group();  // an empty one, so that groups count chunks
             __syncwarp();
           }
         }
