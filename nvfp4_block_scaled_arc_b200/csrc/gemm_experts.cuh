@@ -574,7 +574,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (rr < nrows) {
               __nv_bfloat16* dst = g.y + (y0 + r0 + rr) * g.ldy + f0 + f;
               const uint32_t at16 = static_cast<uint32_t>(2 * (lane & 1)) ^ ((rr >> 1) & 3);
-              const uint4 a = lds_u32x4(stg32 + rr * 64 + 16 * at16), b = lds_u32x4(stg32 + rr * 64 + 16 * (at16 ^ 1));
+              const uint4 a = lds_u32x4(stg32 + rr * 64 + 16 * at16);
+              const uint4 b = lds_u32x4(stg32 + rr * 64 + 16 * (at16 ^ 1));
               if (f0 + f < g.N) *reinterpret_cast<uint4*>(dst) = a;
               if (f0 + f + 8 < g.N) *reinterpret_cast<uint4*>(dst + 8) = b;
             }
