@@ -41,7 +41,10 @@ namespace arc {
 
 // MAXN: rows of a tile, at most. 256 is the general form; 64 (few rows for each expert, where reading the
 // weights is the work) leaves room for more stages in flight and for more accumulators.
-template <int KIND, int MAXN>
+// BATCH: chunks of Y that an epilogue warp stages and stores together, one fence and one wait for all. Shallow
+// products are bound by their epilogue (MXFP4, one accumulator), so that more of them pay for one
+// pipeline stage less; deep ones want the stage.
+template <int KIND, int MAXN, int BATCH>
 struct ExpertGemmTraits {
   static constexpr bool MX4 = KIND == kGemmMX4;
   static constexpr int BM = 128, TM = 256;  // features of a CTA and of the pair
@@ -49,11 +52,7 @@ struct ExpertGemmTraits {
   static constexpr int W_BYTES = BM * 128, X_BYTES = TN / 2 * 128;
   static constexpr int SFW_BYTES = MX4 ? 2 * 512 : 0, SFX_BYTES = MX4 ? TN * 8 : 0;
   static constexpr int STAGE_BYTES = (W_BYTES + X_BYTES + SFW_BYTES + SFX_BYTES + 1023) / 1024 * 1024;
-  static constexpr int STAGES = TN == 256 ? 6 : MX4 ? 9 : 10;
-  // Staging chunks of an epilogue warp, as many as fit: a chunk's store is awaited before its next use. Short
-  // products are bound by their epilogue (32768 rows, 512 -> 4096: BF16 120 us with one chunk, 116 with three;
-  // MXFP4 80 us, and 75 with four chunks and five stages, which costs long products 2 %).
-  static constexpr int EPI_BUFS = TN == 256 ? (MX4 ? 1 : 3) : 2;
+  static constexpr int STAGES = TN == 256 ? (MX4 && BATCH > 1 ? 5 : 6) : MX4 ? 9 : 10;
   static constexpr int ACC_STAGES = TN == 256 ? (MX4 ? 1 : 2) : 3;
   static constexpr int SF_COL0 = ACC_STAGES * TN, SF_SET_COLS = 32;
   static constexpr uint32_t IDESC0 = MX4 ? idesc_mxf4(TM, 0) : idesc_bf16(TM, 0);  // N is the tile's
@@ -73,10 +72,10 @@ constexpr int kExpertBarBytes = 384;
 
 // Shared memory behind the stages: staging, barriers, and every expert's first tile, first row and first
 // block of scale bytes.
-template <int KIND, int MAXN>
+template <int KIND, int MAXN, int BATCH>
 constexpr int expert_gemm_smem_bytes(int experts) {
-  return ExpertGemmTraits<KIND, MAXN>::STAGES * ExpertGemmTraits<KIND, MAXN>::STAGE_BYTES +
-         8 * ExpertGemmTraits<KIND, MAXN>::EPI_BUFS * kExpertEpiBytes +
+  using T = ExpertGemmTraits<KIND, MAXN, BATCH>;
+  return T::STAGES * T::STAGE_BYTES + 8 * BATCH * kExpertEpiBytes +
          kExpertBarBytes + 3 * (experts + 1) * 4 + 1024;
 }
 
@@ -152,11 +151,6 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
           smem_u32(bar)),
       "h"(static_cast<uint16_t>(3))
       : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {  // until at most N groups' sources are still read
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 template <class T>
@@ -236,16 +230,16 @@ __device__ __forceinline__ ExpertTile expert_tile(int t, const int* first, const
   return r;
 }
 
-template <int KIND, int MAXN>
+template <int KIND, int MAXN, int BATCH>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_gemm_experts(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ ExpertRowMaps tmX,
                    const __grid_constant__ CUtensorMap tmY, const ExpertGemmArgs g) {
-  using T = ExpertGemmTraits<KIND, MAXN>;
+  using T = ExpertGemmTraits<KIND, MAXN, BATCH>;
   constexpr bool MX4 = T::MX4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + T::STAGES * T::STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + 8 * T::EPI_BUFS * kExpertEpiBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + 8 * BATCH * kExpertEpiBytes);
   uint64_t* empty = full + T::STAGES;
   uint64_t* ready = empty + T::STAGES;
   uint64_t* acc_full = ready + T::STAGES;
@@ -253,7 +247,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint64_t* drain = acc_empty + T::ACC_STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* first = reinterpret_cast<int*>(staging + 8 * T::EPI_BUFS * kExpertEpiBytes + kExpertBarBytes);  // [E + 1]
+  int* first = reinterpret_cast<int*>(staging + 8 * BATCH * kExpertEpiBytes + kExpertBarBytes);  // [E + 1]
   int* offsets = first + g.experts + 1;                                                          // [E + 1]
   int* blocks = offsets + g.experts + 1;                                                         // [E + 1]
   static_assert((3 * T::STAGES + 2 * T::ACC_STAGES + 1) * 8 + 8 <= kExpertBarBytes, "barriers");
@@ -514,12 +508,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // 8 warps: warp w reads TMEM lane quarter w % 4 (32 features) and every other 16 columns (rows
     // of Y); all of them leave TMEM, rounded, before the first is stored.
     const int q = warp & 3, half = (warp - kGemmEpiWarp0) >> 2;
-    uint8_t* stg0 = staging + (warp - kGemmEpiWarp0) * (T::EPI_BUFS * kExpertEpiBytes);
+    uint8_t* stg = staging + (warp - kGemmEpiWarp0) * (BATCH * kExpertEpiBytes);
+    const uint32_t stg32 = smem_u32(stg);
     // A staged row is 64 bytes, its 16-byte parts permuted by the map's 64-byte swizzle (part ^ (row / 2) % 4),
     // which keeps the eight rows of a matrix on different banks.
-    const uint32_t st_at = (lane & 7) * 64 + 16 * ((lane >> 3) ^ ((lane >> 1) & 3));
+    const uint32_t st_addr = stg32 + (lane & 7) * 64 + 16 * ((lane >> 3) ^ ((lane >> 1) & 3));
     uint32_t acc = 0, acc_phase = 0;
-    int buf = 0;
     for (int t = unit; t < ntiles; t += units) {
       const ExpertTile at = tile(t);
       const int f0 = at.tw * T::TM + static_cast<int>(rank) * T::BM + q * 32;
@@ -548,39 +542,37 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&acc_empty[acc], 0);
+      const int rows = f0 < g.N ? min(at.left, at.n) - 16 * half : 0;  // from the warp's first on
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int r0 = 32 * c + 16 * half;  // first row of the chunk within the tile
-        const int nrows = at.left - r0;
-        if (r0 < at.n && nrows > 0 && f0 < g.N) {
-          uint8_t* stg = stg0 + buf * kExpertEpiBytes;
-          buf = buf + 1 == T::EPI_BUFS ? 0 : buf + 1;
-          const uint32_t stg32 = smem_u32(stg), st_addr = stg32 + st_at;
-          if (lane == 0) bulk_wait_read<T::EPI_BUFS - 1>();  // the store that read this chunk last
-          __syncwarp();
-          stmatrix_x4_trans(st_addr, pk[8 * c], pk[8 * c + 1], pk[8 * c + 2], pk[8 * c + 3]);
-          stmatrix_x4_trans(st_addr + 8 * 64, pk[8 * c + 4], pk[8 * c + 5], pk[8 * c + 6], pk[8 * c + 7]);
-          if (nrows >= 16) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&tmY, stg, f0, static_cast<int32_t>(y0) + r0);  // clipped at the last feature
-              bulk_commit_group();
-            }
-          } else {
-            // the group ends inside these rows: only its own are stored, 16 features a lane
-            __syncwarp();
-            const int rr = lane >> 1, f = 16 * (lane & 1);
-            if (rr < nrows) {
-              __nv_bfloat16* dst = g.y + (y0 + r0 + rr) * g.ldy + f0 + f;
-              const uint32_t at16 = static_cast<uint32_t>(2 * (lane & 1)) ^ ((rr >> 1) & 3);
-              const uint4 a = lds_u32x4(stg32 + rr * 64 + 16 * at16);
-              const uint4 b = lds_u32x4(stg32 + rr * 64 + 16 * (at16 ^ 1));
-              if (f0 + f < g.N) *reinterpret_cast<uint4*>(dst) = a;
-              if (f0 + f + 8 < g.N) *reinterpret_cast<uint4*>(dst + 8) = b;
-            }
-            if (lane == 0) bulk_commit_group();  // an empty one, so that groups count chunks
-            __syncwarp();
+      for (int c0 = 0; c0 < NC; c0 += BATCH) {
+        if (rows <= 32 * c0) break;
+        if (lane < BATCH) bulk_wait_read_all();  // the lane's store of the batch before
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int c = c0 + i;
+          if (32 * c >= rows) break;
+          stmatrix_x4_trans(st_addr + i * kExpertEpiBytes, pk[8 * c], pk[8 * c + 1], pk[8 * c + 2], pk[8 * c + 3]);
+          stmatrix_x4_trans(st_addr + i * kExpertEpiBytes + 8 * 64, pk[8 * c + 4], pk[8 * c + 5], pk[8 * c + 6],
+                            pk[8 * c + 7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane < BATCH && rows - 32 * (c0 + lane) >= 16) {  // clipped at the last feature
+          tma_store_2d(&tmY, stg + lane * kExpertEpiBytes, f0, static_cast<int32_t>(y0) + 32 * (c0 + lane) + 16 * half);
+          bulk_commit_group();
+        }
+        // where the group ends inside a chunk only its own rows are stored, 16 features a lane
+        const int i = (rows >> 5) - c0, nrows = rows & 31;
+        if (i < BATCH && nrows > 0 && nrows < 16) {
+          const int rr = lane >> 1, f = 16 * (lane & 1);
+          if (rr < nrows) {
+            __nv_bfloat16* dst = g.y + (y0 + 32 * (c0 + i) + 16 * half + rr) * g.ldy + f0 + f;
+            const uint32_t src = stg32 + i * kExpertEpiBytes + rr * 64;
+            const uint32_t part = static_cast<uint32_t>(2 * (lane & 1)) ^ ((rr >> 1) & 3);
+            const uint4 a = lds_u32x4(src + 16 * part), b = lds_u32x4(src + 16 * (part ^ 1));
+            if (f0 + f < g.N) *reinterpret_cast<uint4*>(dst) = a;
+            if (f0 + f + 8 < g.N) *reinterpret_cast<uint4*>(dst + 8) = b;
           }
         }
       }
@@ -594,7 +586,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // behind it starts unevenly spread: 23.2 -> 23.8 us). From the kernel's start on it would take the
     // warps' issue slots for the whole product.
     pdl_launch_dependents();
-    if (lane == 0) bulk_wait_all();
+    if (lane < BATCH) bulk_wait_all();
   }
   __syncthreads();
   cluster_sync_all();  // nothing of the pair reads this CTA's memory any more

@@ -70,14 +70,16 @@ arc_status device_check(int* sms) {
                              arc::gemm_smem_bytes<arc::kGemmMX4>()) != cudaSuccess ||
         cudaFuncSetAttribute(arc::k_gemm<arc::kGemmMX4, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              arc::gemm_smem_bytes<arc::kGemmMX4>()) != cudaSuccess ||
-        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             arc::expert_gemm_smem_bytes<arc::kGemmMX4, 64>(arc::kMaxExperts)) != cudaSuccess ||
-        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             arc::expert_gemm_smem_bytes<arc::kGemmMX4, 256>(arc::kMaxExperts)) != cudaSuccess ||
-        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmBF16, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             arc::expert_gemm_smem_bytes<arc::kGemmBF16, 64>(arc::kMaxExperts)) != cudaSuccess ||
-        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmBF16, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             arc::expert_gemm_smem_bytes<arc::kGemmBF16, 256>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4, 64, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmMX4, 64, 2>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4, 256, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmMX4, 256, 1>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmMX4, 256, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmMX4, 256, 4>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmBF16, 64, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmBF16, 64, 2>(arc::kMaxExperts)) != cudaSuccess ||
+        cudaFuncSetAttribute(arc::k_gemm_experts<arc::kGemmBF16, 256, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             arc::expert_gemm_smem_bytes<arc::kGemmBF16, 256, 2>(arc::kMaxExperts)) != cudaSuccess ||
         cudaFuncSetAttribute(arc::k_expert_plan<int32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(arc::plan_smem_bytes(arc::kMaxExperts))) != cudaSuccess ||
         cudaFuncSetAttribute(arc::k_expert_plan<int64_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -496,11 +498,11 @@ arc_status quantize_experts(const void* x, int64_t ldx, int64_t K, const int32_t
                     S(stream), a);
 }
 
-template <int KIND, int MAXN>
+template <int KIND, int MAXN, int BATCH>
 arc_status expert_gemm_launch(const void* a, int64_t a_pitch, const uint8_t* a_sf, const void* b, int64_t b_pitch,
                               const uint8_t* b_sf, const int32_t* plan, int64_t tokens, int32_t k, int32_t experts,
                               int64_t N, int64_t K, void* y, int64_t ldy, arc_stream_t stream) {
-  using T = arc::ExpertGemmTraits<KIND, MAXN>;
+  using T = arc::ExpertGemmTraits<KIND, MAXN, BATCH>;
   constexpr bool MX4 = T::MX4;
   int sms = 0;
   arc_status st = device_check(&sms);
@@ -546,8 +548,8 @@ arc_status expert_gemm_launch(const void* a, int64_t a_pitch, const uint8_t* a_s
                   static_cast<uint32_t>(std::min<int64_t>(arc::row_box_height(i), slots))))
       return ARC_ERR_CUDA;
   g.inject = take_inject(1);
-  return launch_pdl(arc::k_gemm_experts<KIND, MAXN>, 2 * std::min<int64_t>(max_tiles, sms / 2), arc::kGemmThreads,
-                    arc::expert_gemm_smem_bytes<KIND, MAXN>(experts), 2, S(stream), tw, tx, ty, g);
+  return launch_pdl(arc::k_gemm_experts<KIND, MAXN, BATCH>, 2 * std::min<int64_t>(max_tiles, sms / 2), arc::kGemmThreads,
+                    arc::expert_gemm_smem_bytes<KIND, MAXN, BATCH>(experts), 2, S(stream), tw, tx, ty, g);
 }
 
 template <int KIND>
@@ -557,11 +559,19 @@ arc_status expert_gemm(const void* a, int64_t a_pitch, const uint8_t* a_sf, cons
   // Few rows for each expert: 64-row tiles with more stages in flight (one token through 2 of 8
   // experts, BF16 2048 -> 8192: 15.7 against 16.4 us; 32 slots of 64 experts, MXFP4 2048 -> 2048: 17.4
   // against 18.5 us). At 64 rows an expert the wide tiles win (17.2 against 19.2 us, 2036 slots of 32).
-  const bool few = tokens * k <= 32ll * experts;
-  return few ? expert_gemm_launch<KIND, 64>(a, a_pitch, a_sf, b, b_pitch, b_sf, plan, tokens, k, experts, N, K, y, ldy,
-                                            stream)
-             : expert_gemm_launch<KIND, 256>(a, a_pitch, a_sf, b, b_pitch, b_sf, plan, tokens, k, experts, N, K, y,
-                                             ldy, stream);
+  if (tokens * k <= 32ll * experts)
+    return expert_gemm_launch<KIND, 64, 2>(a, a_pitch, a_sf, b, b_pitch, b_sf, plan, tokens, k, experts, N, K, y, ldy,
+                                           stream);
+  // Up to four stages deep: five stages and four chunks staged at once instead of six and one (32768 rows of 8
+  // experts, 512 -> 4096: 64 against 80 us, 1024 -> 4096: 82 against 89 us; level at 2048, and at 4224
+  // 425 against 416 us, 8192 rows -> 28672).
+  if constexpr (KIND == arc::kGemmMX4) {
+    if (K <= 1024)
+      return expert_gemm_launch<KIND, 256, 4>(a, a_pitch, a_sf, b, b_pitch, b_sf, plan, tokens, k, experts, N, K, y,
+                                              ldy, stream);
+  }
+  return expert_gemm_launch<KIND, 256, KIND == arc::kGemmMX4 ? 1 : 2>(a, a_pitch, a_sf, b, b_pitch, b_sf, plan, tokens,
+                                                                      k, experts, N, K, y, ldy, stream);
 }
 
 }  // namespace
