@@ -385,7 +385,9 @@ PRODUCTS = [(1, 2, 8, 64, 8, 0, "skewed"), (1, 8, 64, 512, 264, 32, "skewed"), (
             (64, 4, 32, 1056, 520, 0, "skewed"), (300, 1, 3, 224, 256, 32, "one"), (257, 2, 4, 512, 768, 64, "drop"),
             (600, 2, 2, 4096, 264, 128, "repeat"), (900, 3, 7, 320, 1032, 0, "skewed"),
             (129, 1, 1, 256, 256, 32, "one"), (1500, 2, 5, 1024, 520, 96, "drop"), (40, 6, 512, 128, 72, 0, "drop"),
-            (65, 1, 1, 64, 8, 0, "one"), (257, 1, 1, 32, 128, 0, "one"), (33, 2, 2, 288, 384, 0, "one")]
+            (65, 1, 1, 64, 8, 0, "one"), (257, 1, 1, 32, 128, 0, "one"), (33, 2, 2, 288, 384, 0, "one"),
+            # the most experts with tiles of 256 rows, shallow and deep
+            (2101, 8, 512, 64, 8, 0, "skewed"), (2101, 8, 512, 1056, 40, 32, "drop")]
 
 
 @pytest.mark.parametrize("tokens,k,experts,K,N,r,how", PRODUCTS)
