@@ -619,6 +619,15 @@ __device__ __forceinline__ void expert_places(const QuantExpertsArgs& a, int64_t
   if (dst >= 0 && !plan_place(sfr, a.sf_rows)) dst = -1;
 }
 
+// Sorted rows in use, as the SwiGLU quantizers read them from the plan: a total outside the slots is no
+// plan's, is reported (by one thread of the launch) and counts as none.
+__device__ __forceinline__ int64_t rows_in_use(const QuantExpertsArgs& a, bool report) {
+  const int64_t n = a.p.offsets[a.experts];
+  if (static_cast<uint64_t>(n) <= static_cast<uint64_t>(a.slots)) return n;
+  if (report) set_status(kStatusInvalidArg);
+  return 0;
+}
+
 // Stores block b of a row (the coding of it in this lane) to one destination; every lane of the group
 // calls it with its own block, b >= nblk where it has none.
 __device__ __forceinline__ void store_block(const QuantExpertsArgs& a, int64_t dst, int64_t m, int b, int nblk,
@@ -647,7 +656,7 @@ __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts(QuantExpert
   const int nblk = a.K >> 5, nres = a.r >> 5;
   const int64_t src = blockIdx.x;
   pdl_wait();
-  if (SRC == kQexSwiglu && src >= a.p.offsets[a.experts]) return;
+  if (SRC == kQexSwiglu && src >= rows_in_use(a, src == 0 && threadIdx.x == 0)) return;
   const __nv_bfloat16* row = a.x + src * a.ldx;
   const int nrows = SRC == kQexTokens ? a.k : 1;
   int dst0 = -1, sfr0 = -1;  // lane j: the j-th destination (32 at a time)
@@ -726,7 +735,7 @@ __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts_narrow(Quan
   const int64_t src = (warp << (5 - log_lanes)) + (lane >> log_lanes);
   pdl_wait();
   int64_t n = a.n;
-  if (SRC == kQexSwiglu) n = min(n, static_cast<int64_t>(a.p.offsets[a.experts]));
+  if (SRC == kQexSwiglu) n = rows_in_use(a, src == 0 && l == 0);
   const bool valid = src < n;
   const int nrows = SRC == kQexTokens ? a.k : 1;
   const __nv_bfloat16* row = a.x + src * a.ldx;
