@@ -359,8 +359,8 @@ arc_status arc_combine_experts_bf16(const void* rows_bf16, int64_t ld_rows, int6
 /*
  * Its gradients from d_y [T, d] (the addend's is d_y itself): d_rows [S, d] =
  * bf16(weights[t, j] * d_y[t]) and d_weights fp32 [T, k] (leading dimension ld_dw) =
- * <d_y[t], rows[row]>, fp32 sums in a fixed order; 0 for a slot without a row. d_rows may alias
- * rows.
+ * <d_y[t], rows[row]>, fp32 sums in a fixed order, none a chain of more than max(24, 8 ceil(d / 1024))
+ * products; 0 for a slot without a row. d_rows may alias rows.
  */
 arc_status arc_combine_experts_grad_bf16(const void* d_y_bf16, int64_t ld_dy, const void* rows_bf16, int64_t ld_rows,
                                          int64_t d, const float* weights, int64_t ld_weights, const int32_t* plan,

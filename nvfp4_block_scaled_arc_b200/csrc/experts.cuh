@@ -412,9 +412,11 @@ __global__ void __launch_bounds__(kMoveThreads)
   }
 }
 
-// One group per slot: d_rows[row] = bf16(w d_y[t]) and d_w = <d_y[t], rows[row]> (fp32 partial sums
-// by lane, joined by shuffles: a fixed order). d_rows may be rows: each vector is read before the
-// same lane writes it.
+// One group per slot: d_rows[row] = bf16(w d_y[t]) and d_w = <d_y[t], rows[row]> (an fp32 sum for each of
+// the U vectors of a lane's round, joined by two additions and shuffles: a fixed order; so no chain is
+// longer than max(24, 8 ceil(d / 1024)) products, however few lanes take the row. One sum a lane reached 96
+// and was hardly faster: 45.7 us each at 4096 tokens of 8 x 2048, 59.1 against 60.0 us at 32768 of 8 x 264). d_rows
+// may be rows: each vector is read before the same lane writes it.
 __global__ void __launch_bounds__(kMoveThreads)
     k_combine_grad(const __nv_bfloat16* dy, int64_t lddy, const __nv_bfloat16* rows, int64_t ldr, int vecs,
                    int log_lanes, const float* weights, int64_t ldw, Plan p, int64_t tokens, int k,
@@ -428,13 +430,13 @@ __global__ void __launch_bounds__(kMoveThreads)
   const int64_t t = valid ? s / k : 0, j = s - t * k;
   const int64_t row = valid ? p.row_of_slot[s] : -1;
   const bool has = plan_place(row, slots);
-  float dot = 0.0f;
+  constexpr int U = 4;  // vectors in flight: all loaded before the first is written (rows may be d_rows)
+  float dots[U] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (has) {
     const float w = weights[t * ldw + j];
     const __nv_bfloat16* a = dy + t * lddy;
     const __nv_bfloat16* b = rows + row * ldr;
     uint4* dst = reinterpret_cast<uint4*>(d_rows + row * lddr);
-    constexpr int U = 4;  // vectors in flight: all loaded before the first is written (rows may be d_rows)
     for (int v0 = m.l; v0 < vecs; v0 += lanes * U) {
       uint4 g[U], r[U];
 #pragma unroll
@@ -453,14 +455,15 @@ __global__ void __launch_bounds__(kMoveThreads)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float g0 = bf16_lo(gs[i]), g1 = bf16_hi(gs[i]);
-          dot = __fmaf_rn(g0, bf16_lo(rs[i]), dot);
-          dot = __fmaf_rn(g1, bf16_hi(rs[i]), dot);
+          dots[u] = __fmaf_rn(g0, bf16_lo(rs[i]), dots[u]);
+          dots[u] = __fmaf_rn(g1, bf16_hi(rs[i]), dots[u]);
           o[i] = pack_bf16x2_rn(__fmul_rn(w, g0), __fmul_rn(w, g1));
         }
         if (v0 + lanes * u < vecs) dst[v0 + lanes * u] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
+  float dot = __fadd_rn(__fadd_rn(dots[0], dots[1]), __fadd_rn(dots[2], dots[3]));
   __syncwarp();
   for (int o = lanes >> 1; o; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
   if (valid && m.l == 0) d_w[t * lddw + j] = dot;
