@@ -379,9 +379,12 @@ arc_status arc_quantize_act_experts_mxfp4(const void* x_bf16, int64_t ldx, int64
 
 /*
  * The input of the experts' down projection: sorted rows gu [S, 2F] (gate columns first) give
- * act [S, F] = bf16( silu(gate) * up ), the product formed to about 2^-21 relative (2^-18 for
- * gates near -60) before its one rounding, so it can differ from arc_silu_mul_bf16's by a bf16 step
- * where it lies that near to a rounding border; 0 for gate < -87.3. It is quantized as
+ * act [S, F] = bf16( silu(gate) * up ), the product formed to (1.25 max(-gate, 0) + 9) 2^-24 relative
+ * (2^-20.8 for gate >= 0, 2^-19.7 at -8, 2^-17.6 at -60) before its one rounding, so it can differ from
+ * arc_silu_mul_bf16's by a bf16 step where it lies that near to a rounding border; 0 for gate < -87.3.
+ * (To code arc_silu_mul_bf16's act itself: sort the rows again with a plan of [S, 1] ids, each row's own
+ * expert and -1 behind the last row. They stay where they are, and arc_quantize_act_experts_mxfp4 of act with
+ * that plan writes what a product with the layer's plan reads.) It is quantized as
  * arc_quantize_act_mxfp4 would, with r residual channels of d_idx (channels of act). One kernel; act
  * is not written. Requires F % 32 == 0 and r as above.
  */

@@ -495,11 +495,13 @@ struct QuantExpertsArgs {
 };
 
 // silu(g) * u of a bf16 pair each, rounded to bf16: 2^(-g log2 e), one added, the reciprocal, two
-// products, in fp32 with the approximate 2^x and reciprocal (2 ulp and 1 ulp). The product -g log2 e is
-// off by half an ulp, a relative |g| 2^-24 of the exponential, so the result is good to about 2^-21
-// for g >= -8 and 2^-18 at g = -60 before its one rounding to bf16 (2^-9); below g = -87.3 the
-// reciprocal is flushed and it is 0, where |silu| < 1.1e-36. k_silu_mul's correctly rounded quotient
-// would bound the kernel by its arithmetic (162 against 110 us at 8192 x 14336).
+// products, in fp32 with the approximate 2^x and reciprocal (2 ulp and 1 ulp). Before the one rounding to
+// bf16 (2^-8) the relative error is at most (1.25 max(-g, 0) + 9) 2^-24: the product -g log2 e is off by half
+// an ulp and by log2 e's own rounding, together a relative 1.23 |g| 2^-24 of the exponential; 2^x adds
+// 4 units of 2^-24, the sum 1, the reciprocal 2, the products 2. That is 2^-20.8 at g >= 0, 2^-19.7 at
+// g = -8 and 2^-17.6 at -60, where a value that near to a border between two bf16 values may go to the other
+// one. Below g = -87.3 the reciprocal is flushed and the result is 0, where |silu| < 1.1e-36. k_silu_mul's
+// correctly rounded quotient would bound the kernel by its arithmetic (162 against 110 us at 8192 x 14336).
 __device__ __forceinline__ uint32_t silu_mul_pair(uint32_t g, uint32_t u) {
   const uint64_t g2 = f2_pack(bf16_lo(g), bf16_hi(g));
   constexpr float kNegLog2e = -1.44269504088896341f;

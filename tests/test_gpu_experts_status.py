@@ -18,7 +18,8 @@ def _sections(T, k, E, rows_in_use):
 
 
 # a CTA for each row (few rows, wide rows), and lane groups (many narrow rows); without and with appended blocks
-@pytest.mark.parametrize("T,k,E,F,r", [(16, 2, 4, 64, 0), (3, 1, 2, 2048, 32), (4801, 1, 5, 96, 0), (2400, 2, 5, 512, 64)])
+@pytest.mark.parametrize("T,k,E,F,r", [(16, 2, 4, 64, 0), (3, 1, 2, 2048, 32), (4801, 1, 5, 96, 0),
+                                       (2400, 2, 5, 512, 64)])
 @pytest.mark.parametrize("total", ["negative", "one too many", "huge"])
 def test_a_total_outside_the_slots_is_reported(T, k, E, F, r, total):
     S = T * k
