@@ -436,9 +436,9 @@ MoveShape move_shape(int64_t items, int64_t vecs, int u) {
   m.blocks = (groups + per_block - 1) / per_block;
   return m;
 }
-MoveShape move_shape_fill(int64_t tokens, int64_t vecs, int sm_warps) {
+MoveShape move_shape_fill(int64_t tokens, int64_t vecs, int sms, int sm_warps) {
   const MoveShape four = move_shape(tokens, vecs, 4);
-  return four.blocks * (arc::kMoveThreads / 32) >= 148 * sm_warps ? four : move_shape(tokens, vecs, 1);
+  return four.blocks * (arc::kMoveThreads / 32) >= sms * sm_warps ? four : move_shape(tokens, vecs, 1);
 }
 
 arc_status move_check(int64_t d, int64_t ld_a, int64_t ld_b, const void* a, const void* b, const int32_t* plan,
@@ -839,8 +839,9 @@ arc_status arc_dispatch_experts_bf16(const void* x_bf16, int64_t ldx, int64_t d,
                                      arc_stream_t stream) {
   arc_status st = move_check(d, ldx, ld_rows, x_bf16, rows_bf16, plan, tokens, k, experts);
   if (st != ARC_OK) return st;
-  if ((st = device_check(nullptr)) != ARC_OK) return st;
-  const MoveShape m = move_shape_fill(tokens, d / 8, 32);
+  int sms = 0;
+  if ((st = device_check(&sms)) != ARC_OK) return st;
+  const MoveShape m = move_shape_fill(tokens, d / 8, sms, 32);
   return launch_pdl(m.u == 4 ? arc::k_dispatch<4> : arc::k_dispatch<1>, m.blocks, arc::kMoveThreads, 0, 1, S(stream),
                     static_cast<const __nv_bfloat16*>(x_bf16), ldx, static_cast<int>(d / 8), m.log_lanes, m.nseg,
                     arc::plan_sections(plan, tokens * k, experts), tokens, k, static_cast<__nv_bfloat16*>(rows_bf16),
@@ -850,9 +851,10 @@ arc_status arc_dispatch_experts_bf16(const void* x_bf16, int64_t ldx, int64_t d,
 static arc_status combine_rows(const void* rows, int64_t ld_rows, int64_t d, const float* weights, int64_t ld_weights,
                                const int32_t* plan, int64_t tokens, int32_t k, int32_t experts, const void* add,
                                int64_t ld_add, void* y, int64_t ldy, arc_stream_t stream) {
-  arc_status st = device_check(nullptr);
+  int sms = 0;
+  const arc_status st = device_check(&sms);
   if (st != ARC_OK) return st;
-  const MoveShape m = move_shape_fill(tokens, d / 8, 16);
+  const MoveShape m = move_shape_fill(tokens, d / 8, sms, 16);
   const auto kern = m.log_lanes == 5 ? (m.u == 4 ? arc::k_combine<4, true> : arc::k_combine<1, true>)
                                      : (m.u == 4 ? arc::k_combine<4, false> : arc::k_combine<1, false>);
   return launch_pdl(kern, m.blocks, arc::kMoveThreads, 0, 1, S(stream), static_cast<const __nv_bfloat16*>(rows),
@@ -892,14 +894,15 @@ arc_status arc_combine_experts_grad_bf16(const void* d_y_bf16, int64_t ld_dy, co
     return ARC_ERR_INVALID_ARG;
   if (!al16(d_rows_bf16) || ((reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(d_weights)) & 3u))
     return ARC_ERR_ALIGNMENT;
-  if ((st = device_check(nullptr)) != ARC_OK) return st;
+  int sms = 0;
+  if ((st = device_check(&sms)) != ARC_OK) return st;
   const int64_t slots = tokens * k;
   // One group per slot: lanes that take the row at once where there are few slots, and lanes that take it
   // in up to three rounds, which puts more slots into flight, where there are many (8 choices of 32768
   // x 264: 58 against 78 us, of 4096 x 1536: 35 against 38 us; 64 slots of 1024: 2.8 against 2.1 us).
   const int64_t vecs = d / 8;
   MoveShape m = move_shape(slots, std::min<int64_t>(vecs, 128), 4);
-  if (m.blocks * (arc::kMoveThreads / 32) >= 148 * 16)
+  if (m.blocks * (arc::kMoveThreads / 32) >= sms * 16)
     m = move_shape(slots, std::min<int64_t>(std::max((vecs + 2) / 3, std::min<int64_t>(vecs, 16)), 128), 4);
   return launch_pdl(arc::k_combine_grad, m.blocks, arc::kMoveThreads, 0, 1, S(stream),
                     static_cast<const __nv_bfloat16*>(d_y_bf16), ld_dy, static_cast<const __nv_bfloat16*>(rows_bf16),
