@@ -74,8 +74,8 @@ __device__ __forceinline__ uint32_t ld_u16(const void* p) {
 // memory. Then every warp walks its share of the part, 32 slots at a time, and ranks equal ids by
 // lane (one vote per bit of the id), which keeps the order of slots within an expert: atomics count,
 // none decides a place. Up to 4096 slots one CTA does all. What bounds it is instructions per slot
-// and the latency of a dozen barriers: 3.3 us for 8 slots, 8.6 us for 65536 slots of 64 experts (15.1
-// us with one cluster), 11.2 us for 131072 slots of 256 (28.0 us; 19.7 us in 16 parts).
+// and the latency of a dozen barriers: 3.5 us for 8 slots, 9.0 us for 65536 slots of 64 experts (15.1
+// us with one cluster), 11.7 us for 131072 slots of 256 (28.0 us; 19.7 us in 16 parts).
 // ---------------------------------------------------------------------------------------------
 
 constexpr int kPlanThreads = 1024, kPlanWarps = 32, kPlanCtas = 8, kPlanMaxParts = 8;
@@ -273,8 +273,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 // Sorted rows and back. A group of L lanes (a power of two up to the whole warp, so that narrow rows
 // leave no lane idle) takes one token and a segment of L * U 16-byte vectors of it; a lane holds the
 // place (and weight) of one of L choices at a time, broadcast by shuffle. At 2048 columns the rows
-// move at 0.93 to 0.99 of the copy rate; with 8 choices of 256 columns whole warps reached 0.49 (combine)
-// and 0.30 (its gradient), groups 0.80 and 0.83.
+// move at 0.90 to 1.0 of the copy rate (two choices, the combine: 0.90; eight: 0.96 and more); with 8 choices of
+// 256 columns whole warps reached 0.49 (combine) and 0.32 (its gradient), groups 0.79 and 0.91.
 // ---------------------------------------------------------------------------------------------
 
 constexpr int kMoveThreads = 256;
@@ -339,7 +339,7 @@ __device__ __forceinline__ void fma_bf16x8(float (&acc)[8], float w, uint4 v) {
 // y[t] = bf16( sum_j w_j rows[row_j] [+ add] ): the combine, and with weights of one (weights ==
 // nullptr) the gradient of the dispatch. WHOLE: a group is the warp (16384 tokens of 2 x 4096: 64 us,
 // against 73 us without that branch taken for the warp as a whole). Otherwise several choices'
-// vectors are requested before the first is added (32768 tokens of 8 x 128: 15 against 45 us for a
+// vectors are requested before the first is added (32768 tokens of 8 x 128: 19 against 45 us for a
 // warp per token).
 template <int U, bool WHOLE>
 __global__ void __launch_bounds__(kMoveThreads)
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kQexMaxWarps * 32) k_quant_experts(QuantExpert
 
 // Many rows of at most 32 blocks: a group of 2^log_lanes lanes for each (16 or 32 where there are appended
 // blocks), a block in each lane. With a CTA for each row most lanes of narrow rows idle, and the rows
-// are bound by instructions (16384 rows of 256: 17.5 against 3.7 us, of 512 with r 64: 17.8 against 10.0 us;
+// are bound by instructions (16384 rows of 256: 17.8 against 4.0 us, of 512 with r 64: 18.1 against 11.8 us;
 // 131072 SwiGLU rows: 136 against 30 us and 140 against 78 us).
 // A half warp takes an appended block, a lane two of its channels; the primary blocks' scale bytes come
 // by shuffle. Where a row fills several warps that form is no faster (4096 channels, r 256: 53.5 against

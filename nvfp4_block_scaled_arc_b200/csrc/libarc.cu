@@ -899,7 +899,7 @@ arc_status arc_combine_experts_grad_bf16(const void* d_y_bf16, int64_t ld_dy, co
   const int64_t slots = tokens * k;
   // One group per slot: lanes that take the row at once where there are few slots, and lanes that take it
   // in up to three rounds, which puts more slots into flight, where there are many (8 choices of 32768
-  // x 264: 58 against 78 us, of 4096 x 1536: 35 against 38 us; 64 slots of 1024: 2.8 against 2.1 us).
+  // x 264: 59 against 80 us, of 4096 x 1536: 36 against 39 us; 64 slots of 1024: 2.8 against 2.1 us).
   const int64_t vecs = d / 8;
   MoveShape m = move_shape(slots, std::min<int64_t>(vecs, 128), 4);
   if (m.blocks * (arc::kMoveThreads / 32) >= sms * 16)
